@@ -125,7 +125,7 @@ def _quantize(x, bits, dim):
     """(codes, scale, zero) of fp32 x with statistics over dim (kept)."""
     M = (1 << bits) - 1
     mn, mx = x.amin(dim, keepdim=True) + 0.0, x.amax(dim, keepdim=True) + 0.0
-    scale = (mx - mn) / M
+    scale = (mx - mn) / torch.full_like(mx, M)          # a quotient: a Python divisor would become a product
     code = torch.round((x - mn) / torch.where(scale == 0, 1.0, scale)).clamp(0, M)
     return torch.where(scale == 0, 0.0, code).int(), scale, mn
 
