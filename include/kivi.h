@@ -289,6 +289,107 @@ int32_t kivi_decode_pv_noalloc(const kivi_cache* c, const float* logits,
                                int32_t ld_logits, int32_t Hq, float* out,
                                void* stream);
 
+/* ------------------------------------- speculative and sparse decoding ---- */
+
+/*
+ * The pages have no counterpart of the calls in this section: they serve a
+ * decode loop that verifies several drafted tokens at once, or that reads only
+ * the part of a long cache its query attends to.  Both attentions run over the
+ * values that kivi_dequant materializes (K_hat, V_hat = x_hat of the codes,
+ * fp16 residual tokens as they are), with fp32 sums and softmax statistics.
+ * A sequence's len[b] is read on the device and taken as min(len[b], Tmax)
+ * (0 if negative).
+ */
+
+/* Largest number of drafted tokens of one kivi_tree_attention call. */
+#define KIVI_MAX_DRAFT 256
+
+/*
+ * Choose the key groups a query may attend.  A group's smallest and largest
+ * key are its statistics, lo_d = zero_d and hi_d = zero_d + M scale_d (an fp32
+ * product, then an fp32 sum), so
+ *   bound(hq, g) = sum_d max(q_d lo_d, q_d hi_d)
+ * is at least q . K_hat_t for every token t of group g, and no codes are read.
+ *   scores[b][h][g] = max over the Hq/H query heads of KV head h of bound
+ * for the Tq/G quantized groups; entries past them are not written.  The
+ * arithmetic is fp32 and its order fixed -- each product rounded, then sums of
+ * neighbouring channels, of neighbouring pairs, and so on -- so that scores and
+ * choice are the same bit for bit from run to run and on any implementation.
+ *   blocks[b][h][0 .. n_keep) = the indices of the min(n_keep, Tq/G) groups of
+ * largest score, the lower index first among equal scores (a NaN counts as the
+ * lowest), in ascending order, then -1.
+ * q: fp16 [B][Hq][D]; blocks: int32 [B][H][n_keep], n_keep >= 1; scores: fp32
+ * [B][H][Tmax/G].  Hq as for kivi_decode_qk.  Two kernels on `stream`.
+ */
+int32_t kivi_block_select(const kivi_cache* c, const uint16_t* q, int32_t Hq,
+                          int32_t* blocks, int32_t n_keep, float* scores,
+                          void* stream);
+
+/*
+ * Decode attention over the listed key groups and the residual:
+ *   out[b][hq][d] = sum_t softmax_t(sm_scale q . K_hat_t) V_hat[t][d]
+ * over the tokens t of the groups blocks[b][h][i], i < min(n_keep, Tq/G), and
+ * over all residual tokens Tq <= t < len[b].  Entries outside [0, Tq/G) are
+ * skipped; a group listed twice counts twice.  Any order is accepted; lists of
+ * kivi_block_select are ascending.  q: fp16 [B][Hq][D]; blocks: int32
+ * [B][H][n_keep], n_keep >= 1; out: fp32 [B][Hq][D]; ws: device, >=
+ * kivi_attend_workspace_bytes(c, Hq, 1) bytes, 16-byte aligned, contents need
+ * not be initialized.  A row without any token gets out = 0.  The first 4
+ * bytes of ws receive a status word: KIVI_OK, or KIVI_ETIMEOUT if a bounded
+ * wait inside the kernel gave up (the outputs are then invalid).  Calls that
+ * share a workspace must not overlap on the GPU.  The work split and every
+ * sum's order depend only on the sizes and lengths: the same inputs give the
+ * same bits.
+ */
+int32_t kivi_sparse_attention(const kivi_cache* c, const uint16_t* q,
+                              int32_t Hq, float sm_scale,
+                              const int32_t* blocks, int32_t n_keep,
+                              float* out, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Attention of N drafted tokens per sequence -- a token tree, a chain, or any
+ * other set -- over the cache and one another:
+ *   out[b][hq][i][d] = sum_t softmax_t(sm_scale q_i . K_t) V_t[d]
+ * over all len[b] cached tokens and the drafted tokens j whose bit j % 64 of
+ * word mask[b][i][j / 64] is set.  Neither the cache nor its lengths change;
+ * kivi_append_path then keeps the accepted tokens.  q: fp16 [B][Hq][N][D];
+ * k, v: fp16 [B][H][N][D]; mask: uint64 [B][N][ceil(N/64)]; out: fp32
+ * [B][Hq][N][D]; 1 <= N <= KIVI_MAX_DRAFT.  n_draft (device int32 [B], or NULL
+ * for N everywhere) gives the drafted tokens of each sequence, taken as
+ * min(n_draft[b], N) (0 if negative): k, v and mask bits of tokens from there
+ * on are not read, and their rows of out are left as they were.  A row that
+ * attends nothing gets out = 0.  ws: as for kivi_sparse_attention, >=
+ * kivi_attend_workspace_bytes(c, Hq, N) bytes; status word, sharing and
+ * determinism as there.
+ */
+int32_t kivi_tree_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq,
+                            int32_t N, const uint16_t* k, const uint16_t* v,
+                            const uint64_t* mask, const int32_t* n_draft,
+                            float sm_scale, float* out, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * Workspace bytes of kivi_tree_attention for N drafted tokens and, with N = 1,
+ * of kivi_sparse_attention.  Host only; 0 for invalid sizes.
+ */
+size_t kivi_attend_workspace_bytes(const kivi_cache* c, int32_t Hq, int32_t N);
+
+/*
+ * Append the accepted tokens of a draft: tokens path[b][0 .. counts[b]) of k,
+ * v (fp16 [B][H][N][D]) become tokens len[b] .. of sequence b, exactly as
+ * counts[b] calls of kivi_append_token would append them (ring slots, group
+ * flushes, len[b]).  path: int32 [B][P]; counts: int32 [B]; 1 <= N, P.
+ * A sequence is left unchanged and *status (device int32) set if counts[b] is
+ * outside [0, P] or one of its path entries outside [0, N) (KIVI_EINVAL), or
+ * if it would exceed Tmax (KIVI_ECAPACITY); *status is otherwise not written.
+ * The same token may appear twice on a path.  Two kernels on `stream`.
+ */
+int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k,
+                         const uint16_t* v, int32_t N, const int32_t* path,
+                         int32_t P, const int32_t* counts, int32_t* status,
+                         void* stream);
+
 /* ------------------------------------------------ compact payload (store) */
 
 /*

@@ -36,7 +36,8 @@ EXPORTS = (
     "kivi_dequant", "kivi_append_token", "kivi_decode_qk", "kivi_decode_pv",
     "kivi_workspace_bytes", "kivi_decode_pv_noalloc", "kivi_decode_attention",
     "kivi_codec_fingerprint", "kivi_payload_bytes", "kivi_export", "kivi_import",
-    "kivi_check_status",
+    "kivi_check_status", "kivi_block_select", "kivi_sparse_attention", "kivi_tree_attention",
+    "kivi_attend_workspace_bytes", "kivi_append_path",
 )
 
 KIVI_PAYLOAD_MAGIC = 0x5056494B
@@ -44,6 +45,8 @@ KIVI_PAYLOAD_VERSION = 1
 KIVI_PAYLOAD_HEADER_BYTES = 64
 
 KIVI_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
+
+KIVI_MAX_DRAFT = 256
 
 
 class KiviError(RuntimeError):
@@ -100,6 +103,11 @@ def load(path: str | None = None):
         "kivi_export": ([cp, vp, sz, vp, vp], i32),
         "kivi_import": ([cp, vp, sz, vp, vp], i32),
         "kivi_check_status": ([C.POINTER(i32)], i32),
+        "kivi_block_select": ([cp, vp, i32, vp, i32, vp, vp], i32),
+        "kivi_sparse_attention": ([cp, vp, i32, f32, vp, i32, vp, vp, sz, vp], i32),
+        "kivi_tree_attention": ([cp, vp, i32, i32, vp, vp, vp, vp, f32, vp, vp, sz, vp], i32),
+        "kivi_attend_workspace_bytes": ([cp, i32, i32], sz),
+        "kivi_append_path": ([cp, vp, vp, i32, vp, i32, vp, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -178,6 +186,10 @@ def kivi_payload_bytes(desc: kivi_cache, lens) -> int:
 
 def kivi_workspace_bytes(cache, Hq: int) -> int:
     return int(load().kivi_workspace_bytes(C.byref(cache.desc), Hq))
+
+
+def kivi_attend_workspace_bytes(cache, Hq: int, N: int = 1) -> int:
+    return int(load().kivi_attend_workspace_bytes(C.byref(cache.desc), Hq, N))
 
 
 # ---------------------------------------------------------- device calls ---
@@ -287,6 +299,106 @@ def kivi_decode_attention(cache, q: torch.Tensor, out: torch.Tensor, ws: torch.T
                                         Hq, sm, _dev(out, torch.float32, "out", cache.device), wp,
                                         ws.numel() * ws.element_size(), _stream(stream, cache.device)),
            "kivi_decode_attention")
+
+
+def _shape(t: torch.Tensor, name: str, *shapes):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) not in shapes:
+        raise ValueError(f"{name} shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
+
+
+def _ws(ws: torch.Tensor, device):
+    return _dev(ws, ws.dtype, "ws", device), ws.numel() * ws.element_size()
+
+
+def kivi_block_select(cache, q: torch.Tensor, blocks: torch.Tensor, scores: torch.Tensor, stream=None):
+    """blocks int32 [B, H, n_keep] <- the quantized key groups of largest score,
+    ascending and padded with -1; scores fp32 [B, H, Tmax/G] <- the scores, an
+    upper bound of q . k over each group; q fp16 [B, Hq, D] (or [B, Hq, 1, D])."""
+    B, H, D = cache.B, cache.H, cache.D
+    Hq = q.shape[1] if q.dim() > 1 else 0
+    _shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
+    n_keep = blocks.shape[-1] if blocks.dim() else 0
+    _shape(blocks, "blocks", (B, H, n_keep))
+    _shape(scores, "scores", (B, H, cache.Tmax // cache.G))
+    dev = cache.device
+    _check(load().kivi_block_select(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq,
+                                    _dev(blocks, torch.int32, "blocks", dev), n_keep,
+                                    _dev(scores, torch.float32, "scores", dev), _stream(stream, dev)),
+           "kivi_block_select")
+
+
+def kivi_sparse_attention(cache, q: torch.Tensor, blocks: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                          sm_scale: float | None = None, stream=None):
+    """out fp32 [B, Hq, D] <- decode attention of q fp16 [B, Hq, D] (or
+    [B, Hq, 1, D]) over the key groups blocks int32 [B, H, n_keep] lists and
+    the fp16 residual; ws of at least kivi_attend_workspace_bytes(cache, Hq)."""
+    B, H, D = cache.B, cache.H, cache.D
+    Hq = q.shape[1] if q.dim() > 1 else 0
+    _shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
+    n_keep = blocks.shape[-1] if blocks.dim() else 0
+    _shape(blocks, "blocks", (B, H, n_keep))
+    _shape(out, "out", (B, Hq, D), (B, Hq, 1, D))
+    sm = float(D ** -0.5) if sm_scale is None else float(sm_scale)
+    dev = cache.device
+    wp, wb = _ws(ws, dev)
+    _check(load().kivi_sparse_attention(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq, sm,
+                                        _dev(blocks, torch.int32, "blocks", dev), n_keep,
+                                        _dev(out, torch.float32, "out", dev), wp, wb, _stream(stream, dev)),
+           "kivi_sparse_attention")
+
+
+def kivi_tree_attention(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor,
+                        out: torch.Tensor, ws: torch.Tensor, n_draft: torch.Tensor | None = None,
+                        sm_scale: float | None = None, stream=None):
+    """out fp32 [B, Hq, N, D] <- attention of N drafted tokens q fp16
+    [B, Hq, N, D] over the cache and the drafts k, v fp16 [B, H, N, D] that
+    mask int64 [B, N, ceil(N/64)] allows (bit j % 64 of word j // 64 of row i:
+    token i attends token j).  n_draft int32 [B]: tokens each sequence drafted
+    (rows from there on keep their contents); ws of at least
+    kivi_attend_workspace_bytes(cache, Hq, N)."""
+    B, H, D = cache.B, cache.H, cache.D
+    Hq, N = (q.shape[1], q.shape[2]) if q.dim() == 4 else (0, 0)
+    _shape(q, "q", (B, Hq, N, D))
+    _shape(k, "k", (B, H, N, D))
+    _shape(v, "v", (B, H, N, D))
+    _shape(mask, "mask", (B, N, (N + 63) // 64))
+    _shape(out, "out", (B, Hq, N, D))
+    dev = cache.device
+    if n_draft is not None:
+        _shape(n_draft, "n_draft", (B,))
+    sm = float(D ** -0.5) if sm_scale is None else float(sm_scale)
+    wp, wb = _ws(ws, dev)
+    _check(load().kivi_tree_attention(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq, N,
+                                      _dev(k, torch.float16, "k", dev), _dev(v, torch.float16, "v", dev),
+                                      _dev(mask, torch.int64, "mask", dev),
+                                      None if n_draft is None else _dev(n_draft, torch.int32, "n_draft", dev),
+                                      sm, _dev(out, torch.float32, "out", dev), wp, wb, _stream(stream, dev)),
+           "kivi_tree_attention")
+
+
+def kivi_append_path(cache, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor, counts: torch.Tensor,
+                     status: torch.Tensor, stream=None):
+    """Append the drafted tokens path[b, :counts[b]] (path int32 [B, P], counts
+    int32 [B]) of k, v fp16 [B, H, N, D] to every sequence.  A sequence with a
+    bad count or path entry, or without room, is left as it was and status[0]
+    set on the device (KIVI_EINVAL, KIVI_ECAPACITY)."""
+    B, H, D = cache.B, cache.H, cache.D
+    N = k.shape[2] if k.dim() == 4 else 0
+    _shape(k, "k", (B, H, N, D))
+    _shape(v, "v", (B, H, N, D))
+    P = path.shape[-1] if path.dim() else 0
+    _shape(path, "path", (B, P))
+    _shape(counts, "counts", (B,))
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    dev = cache.device
+    _check(load().kivi_append_path(C.byref(cache.desc), _dev(k, torch.float16, "k", dev),
+                                   _dev(v, torch.float16, "v", dev), N, _dev(path, torch.int32, "path", dev), P,
+                                   _dev(counts, torch.int32, "counts", dev),
+                                   _dev(status, torch.int32, "status", dev), _stream(stream, dev)),
+           "kivi_append_path")
 
 
 def _payload_buf(t: torch.Tensor, name: str, device) -> int:

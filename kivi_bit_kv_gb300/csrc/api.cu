@@ -333,6 +333,129 @@ int32_t kivi_decode_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq
                                                   (cudaStream_t)stream));
 }
 
+// ----------------------------------------- speculative and sparse decode ---
+
+// The kernels run on the current device: refuse a cache that lives on another.
+static int32_t check_current_device(const kivi_cache* c)
+{
+    cudaPointerAttributes a;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, c->kq) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(KIVI_ECUDA, "the current device or the cache's memory could not be queried");
+    }
+    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+        return fail(KIVI_EINVAL, "cache buffer kq is not device memory");
+    if (a.type == cudaMemoryTypeDevice && a.device != dev)
+        return fail(KIVI_EINVAL, "the cache is on device %d, the current device is %d", a.device, dev);
+    return KIVI_OK;
+}
+
+static int32_t check_blocks(const kivi_cache* c, const int32_t* blocks, int32_t n_keep)
+{
+    if (n_keep < 1)
+        return fail(KIVI_EINVAL, "n_keep=%d must be >= 1", n_keep);
+    return check_ptr(blocks, "blocks");
+}
+
+int32_t kivi_block_select(const kivi_cache* c, const uint16_t* q, int32_t Hq, int32_t* blocks, int32_t n_keep,
+                          float* scores, void* stream)
+{
+    NvtxRange range_("kivi_block_select");
+    int32_t st = check_cache(c);
+    if (st != KIVI_OK || (st = check_heads(c, Hq)) != KIVI_OK || (st = check_ptr(q, "q")) != KIVI_OK ||
+        (st = check_blocks(c, blocks, n_keep)) != KIVI_OK || (st = check_ptr(scores, "scores")) != KIVI_OK ||
+        (st = check_current_device(c)) != KIVI_OK)
+        return st;
+    return launched(kivi::launch_block_select(*c, q, Hq, blocks, n_keep, scores, (cudaStream_t)stream));
+}
+
+size_t kivi_attend_workspace_bytes(const kivi_cache* c, int32_t Hq, int32_t N)
+{
+    if (check_sizes(c) != KIVI_OK || check_heads(c, Hq) != KIVI_OK || N < 1 || N > KIVI_MAX_DRAFT)
+        return 0;
+    return kivi::attend_ws_bytes(*c, Hq, N);
+}
+
+static int32_t check_attend_ws(const kivi_cache* c, int32_t Hq, int32_t N, const float* out, const void* ws,
+                               size_t ws_bytes_given)
+{
+    int32_t st;
+    if ((st = check_ptr(out, "out")) != KIVI_OK || (st = check_ptr(ws, "ws")) != KIVI_OK)
+        return st;
+    const size_t need = kivi::attend_ws_bytes(*c, Hq, N);
+    if (ws_bytes_given < need)
+        return fail(KIVI_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes_given, need);
+    return check_current_device(c);
+}
+
+int32_t kivi_sparse_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq, float sm_scale,
+                              const int32_t* blocks, int32_t n_keep, float* out, void* ws,
+                              size_t ws_bytes_given, void* stream)
+{
+    NvtxRange range_("kivi_sparse_attention");
+    int32_t st = check_cache(c);
+    if (st != KIVI_OK || (st = check_heads(c, Hq)) != KIVI_OK || (st = check_ptr(q, "q")) != KIVI_OK ||
+        (st = check_blocks(c, blocks, n_keep)) != KIVI_OK ||
+        (st = check_attend_ws(c, Hq, 1, out, ws, ws_bytes_given)) != KIVI_OK)
+        return st;
+    kivi::AttendArgs a = {};
+    a.q = q;
+    a.Hq = Hq;
+    a.N = 1;
+    a.blocks = blocks;
+    a.n_keep = n_keep;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    return launched(kivi::launch_attend(*c, a, ws, (cudaStream_t)stream));
+}
+
+int32_t kivi_tree_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq, int32_t N, const uint16_t* k,
+                            const uint16_t* v, const uint64_t* mask, const int32_t* n_draft, float sm_scale,
+                            float* out, void* ws, size_t ws_bytes_given, void* stream)
+{
+    NvtxRange range_("kivi_tree_attention");
+    int32_t st = check_cache(c);
+    if (st != KIVI_OK || (st = check_heads(c, Hq)) != KIVI_OK)
+        return st;
+    if (N < 1 || N > KIVI_MAX_DRAFT)
+        return fail(KIVI_EINVAL, "N=%d drafted tokens; valid: 1 .. %d", N, KIVI_MAX_DRAFT);
+    if ((st = check_ptr(q, "q")) != KIVI_OK || (st = check_ptr(k, "k")) != KIVI_OK ||
+        (st = check_ptr(v, "v")) != KIVI_OK || (st = check_ptr(mask, "mask")) != KIVI_OK)
+        return st;
+    if (n_draft && ((uintptr_t)n_draft & 3u))
+        return fail(KIVI_EINVAL, "n_draft is not 4-byte aligned");
+    if ((st = check_attend_ws(c, Hq, N, out, ws, ws_bytes_given)) != KIVI_OK)
+        return st;
+    kivi::AttendArgs a = {};
+    a.q = q;
+    a.Hq = Hq;
+    a.N = N;
+    a.k = k;
+    a.v = v;
+    a.mask = mask;
+    a.n_draft = n_draft;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    return launched(kivi::launch_attend(*c, a, ws, (cudaStream_t)stream));
+}
+
+int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k, const uint16_t* v, int32_t N,
+                         const int32_t* path, int32_t P, const int32_t* counts, int32_t* status, void* stream)
+{
+    NvtxRange range_("kivi_append_path");
+    int32_t st = check_cache(c);
+    if (st != KIVI_OK)
+        return st;
+    if (N < 1 || P < 1)
+        return fail(KIVI_EINVAL, "N=%d P=%d: both must be >= 1", N, P);
+    if ((st = check_ptr(k, "k")) != KIVI_OK || (st = check_ptr(v, "v")) != KIVI_OK ||
+        (st = check_ptr(path, "path", false)) != KIVI_OK || (st = check_ptr(counts, "counts", false)) != KIVI_OK ||
+        (st = check_ptr(status, "status", false)) != KIVI_OK || (st = check_current_device(c)) != KIVI_OK)
+        return st;
+    return launched(kivi::launch_append_path(*c, k, v, N, path, P, counts, status, (cudaStream_t)stream));
+}
+
 // ------------------------------------------------------ compact payload ---
 
 uint64_t kivi_codec_fingerprint(const kivi_cache* c)
@@ -417,7 +540,8 @@ int32_t kivi_check_status(int32_t* status)
     const int32_t words[] = {kivi::check_word_quant(),    kivi::check_word_dequant(),
                              kivi::check_word_append(),   kivi::check_word_payload(),
                              kivi::check_word_decode(),   kivi::check_word_decode_d64(),
-                             kivi::check_word_decode_d128(), kivi::check_word_decode_d256()};
+                             kivi::check_word_decode_d128(), kivi::check_word_decode_d256(),
+                             kivi::check_word_select(),   kivi::check_word_attend()};
     for (const int32_t w : words) {
         if (w == KIVI_ECUDA)
             return fail(KIVI_ECUDA, "reading the device check words failed");

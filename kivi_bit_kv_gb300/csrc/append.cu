@@ -129,6 +129,122 @@ cudaError_t launch_append(const kivi_cache& c, const uint16_t* k, const uint16_t
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------ append path ---
+
+// Status of appending the first n = counts[b] nodes of path row b to a
+// sequence of L tokens; every thread of the warp calls it and gets the result.
+__device__ __forceinline__ int path_status(const kivi_cache& c, int L, int n, const int32_t* row, int N, int P)
+{
+    if (L < 0 || n < 0 || n > P)
+        return KIVI_EINVAL;
+    bool bad = false;
+    for (int i = threadIdx.x & 31; i < n; i += 32) {
+        const int node = ldg_checked(row + i);
+        bad |= node < 0 || node >= N;
+    }
+    if (__any_sync(0xffffffffu, bad))
+        return KIVI_EINVAL;
+    return (long long)L + n > c.Tmax ? KIVI_ECAPACITY : KIVI_OK;
+}
+
+// One CTA per (b, h).  The accepted tokens enter the ring in runs that end
+// where the residual reaches R + G; there the oldest G tokens are flushed as
+// append_kernel flushes them, and the next run reuses their slots.  Bound by
+// latency: a dependent chain of length, path and token loads, then one store
+// (16 x 8 B of D = 128 channels per token and head).
+template <int BK, int BV>
+__global__ void __launch_bounds__(128)
+append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int N,
+                   const int32_t* __restrict__ path, int P, const int32_t* __restrict__ counts, int32_t* status)
+{
+    const size_t bh = blockIdx.x;
+    const int b = (int)(bh / c.H), h = (int)(bh % c.H);
+    const int L = ld_checked(c.len + b);
+    const int n = ldg_checked(counts + b);
+    const int32_t* row = path + (size_t)b * P;
+    const int st = path_status(c, L, n, row, N, P);
+    if (st != KIVI_OK) {  // uniform over the CTA
+        if (h == 0 && threadIdx.x == 0)
+            atomicExch(status, st);
+        return;
+    }
+    const int D = c.D, G = c.G, RG = c.R + c.G, NC = D / kLaneChans;
+    for (int done = 0; done < n;) {
+        const int Tq = quantized_tokens(L + done, G, c.R);
+        const int res = L + done - Tq;  // < R + G
+        const int m = min(RG - res, n - done);
+        for (int i = threadIdx.x; i < m * NC; i += blockDim.x) {
+            const int j = i / NC, ch = (i % NC) * kLaneChans;
+            const size_t o = (bh * RG + (L + done + j) % RG) * D + ch;
+            const size_t in = (bh * N + ldg_checked(row + done + j)) * D + ch;
+            st_checked(reinterpret_cast<uint4*>(c.kres + o), ldg_checked(reinterpret_cast<const uint4*>(k + in)));
+            st_checked(reinterpret_cast<uint4*>(c.vres + o), ldg_checked(reinterpret_cast<const uint4*>(v + in)));
+        }
+        done += m;
+        if (res + m == RG) {
+            __syncthreads();  // the ring is full and visible to every thread of the CTA
+            switch (G) {
+            case 32:
+                flush_keys<BK, 2>(c, bh, Tq);
+                flush_values<BV, 32>(c, bh, Tq);
+                break;
+            case 64:
+                flush_keys<BK, 4>(c, bh, Tq);
+                flush_values<BV, 64>(c, bh, Tq);
+                break;
+            default:
+                flush_keys<BK, 8>(c, bh, Tq);
+                flush_values<BV, 128>(c, bh, Tq);
+                break;
+            }
+            __syncthreads();  // the flushed slots are read before the next run reuses them
+        }
+    }
+}
+
+// One warp per sequence: adds the tokens append_path_kernel appended.
+__global__ void __launch_bounds__(128)
+advance_path_kernel(kivi_cache c, int N, const int32_t* __restrict__ path, int P,
+                    const int32_t* __restrict__ counts)
+{
+    const int b = (int)(blockIdx.x * 4 + threadIdx.x / 32);
+    if (b >= c.B)
+        return;
+    const int L = ld_checked(c.len + b), n = ldg_checked(counts + b);
+    const int st = path_status(c, L, n, path + (size_t)b * P, N, P);
+    __syncwarp();
+    if (st == KIVI_OK && (threadIdx.x & 31) == 0)
+        st_checked(c.len + b, L + n);
+}
+
+template <int BK>
+static void launch_append_path_bk(const kivi_cache& c, const uint16_t* k, const uint16_t* v, int N,
+                                  const int32_t* path, int P, const int32_t* counts, int32_t* status,
+                                  cudaStream_t s)
+{
+    const dim3 grid(c.B * c.H);
+    switch (c.bits_v) {
+    case 2: append_path_kernel<BK, 2><<<grid, 128, 0, s>>>(c, k, v, N, path, P, counts, status); break;
+    case 4: append_path_kernel<BK, 4><<<grid, 128, 0, s>>>(c, k, v, N, path, P, counts, status); break;
+    default: append_path_kernel<BK, 8><<<grid, 128, 0, s>>>(c, k, v, N, path, P, counts, status); break;
+    }
+}
+
+cudaError_t launch_append_path(const kivi_cache& c, const uint16_t* k, const uint16_t* v, int N,
+                               const int32_t* path, int P, const int32_t* counts, int32_t* status,
+                               cudaStream_t s)
+{
+    KIVI_SET_CHECK_RANGES(c, s, {{k, (size_t)c.B * c.H * N * c.D * 2}, {v, (size_t)c.B * c.H * N * c.D * 2},
+                                 {path, (size_t)c.B * P * 4}, {counts, (size_t)c.B * 4}, {status, 4}});
+    switch (c.bits_k) {
+    case 2: launch_append_path_bk<2>(c, k, v, N, path, P, counts, status, s); break;
+    case 4: launch_append_path_bk<4>(c, k, v, N, path, P, counts, status, s); break;
+    default: launch_append_path_bk<8>(c, k, v, N, path, P, counts, status, s); break;
+    }
+    advance_path_kernel<<<(c.B + 3) / 4, 128, 0, s>>>(c, N, path, P, counts);
+    return cudaGetLastError();
+}
+
 #ifdef KIVI_CHECKS
 int32_t check_word_append() { return take_check_word(); }
 #endif

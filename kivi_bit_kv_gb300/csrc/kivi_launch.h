@@ -23,6 +23,28 @@ cudaError_t launch_dequant(const kivi_cache& c, int which, uint16_t* out, int T_
                            cudaStream_t s);
 cudaError_t launch_append(const kivi_cache& c, const uint16_t* k, const uint16_t* v,
                           int32_t* status, cudaStream_t s);
+cudaError_t launch_append_path(const kivi_cache& c, const uint16_t* k, const uint16_t* v, int N,
+                               const int32_t* path, int P, const int32_t* counts, int32_t* status,
+                               cudaStream_t s);
+// Scores of the quantized groups and the n_keep best of each (b, h).
+cudaError_t launch_block_select(const kivi_cache& c, const uint16_t* q, int Hq, int32_t* blocks, int n_keep,
+                                float* scores, cudaStream_t s);
+// Attention of N query tokens per sequence over the cache: all of it and the
+// drafted tokens (blocks NULL), or the listed key groups and the residual
+// (N = 1, k NULL).
+struct AttendArgs {
+    const uint16_t* q;       // [B][Hq][N][D]
+    const uint16_t* k;       // [B][H][N][D] or NULL
+    const uint16_t* v;
+    const uint64_t* mask;    // [B][N][ceil(N/64)]
+    const int32_t* n_draft;  // [B] or NULL
+    const int32_t* blocks;   // [B][H][n_keep] or NULL
+    float* out;              // [B][Hq][N][D]
+    float sm_scale;
+    int32_t Hq, N, n_keep;
+};
+cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cudaStream_t s);
+size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N);
 cudaError_t launch_decode_qk(const kivi_cache& c, const uint16_t* q, int Hq, float sm_scale,
                              float* logits, int ld_logits, cudaStream_t s);
 // ws_o: [B*Hq][nchunks][D], ws_m / ws_l: [B*Hq][nchunks] (fp32).
@@ -76,6 +98,8 @@ int32_t check_word_decode();
 int32_t check_word_decode_d64();
 int32_t check_word_decode_d128();
 int32_t check_word_decode_d256();
+int32_t check_word_select();
+int32_t check_word_attend();
 #endif
 
 // Sets the message kivi_last_error() returns on this host thread; returns status.
