@@ -44,6 +44,9 @@ struct AttendArgs {
     int32_t Hq, N, n_keep;
 };
 cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cudaStream_t s);
+// The same for one head dimension; instantiated in attend_d<D>.cu.
+template <int D>
+cudaError_t launch_attend_d(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s);
 size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N);
 cudaError_t launch_decode_qk(const kivi_cache& c, const uint16_t* q, int Hq, float sm_scale,
                              float* logits, int ld_logits, cudaStream_t s);
@@ -99,7 +102,9 @@ int32_t check_word_decode_d64();
 int32_t check_word_decode_d128();
 int32_t check_word_decode_d256();
 int32_t check_word_select();
-int32_t check_word_attend();
+int32_t check_word_attend_d64();
+int32_t check_word_attend_d128();
+int32_t check_word_attend_d256();
 #endif
 
 // Sets the message kivi_last_error() returns on this host thread; returns status.
