@@ -541,8 +541,7 @@ int32_t kivi_check_status(int32_t* status)
                              kivi::check_word_append(),   kivi::check_word_payload(),
                              kivi::check_word_decode(),   kivi::check_word_decode_d64(),
                              kivi::check_word_decode_d128(), kivi::check_word_decode_d256(),
-                             kivi::check_word_select(),   kivi::check_word_attend_d64(),
-                             kivi::check_word_attend_d128(), kivi::check_word_attend_d256()};
+                             kivi::check_word_select(),   kivi::check_word_attend()};
     for (const int32_t w : words) {
         if (w == KIVI_ECUDA)
             return fail(KIVI_ECUDA, "reading the device check words failed");

@@ -1,6 +1,7 @@
 // attend.cu -- dispatch of kivi_sparse_attention and kivi_tree_attention
-// (kernels in attend.cuh, one translation unit per head dimension).
-#include "attend.cuh"
+// (kernels in attend.cuh, one translation unit per head dimension and width).
+#include "attend_plan.h"
+#include "kivi_launch.h"
 
 namespace kivi {
 
@@ -9,6 +10,17 @@ size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N)
     const int NR = attend_rows(c.D, Hq / c.H * N);
     return ((size_t)kAttHeaderFloats + (size_t)kAttMaxCTAs * kAttCutInts +
             (size_t)kAttMaxCTAs * 2 * NR * (c.D + 2)) * sizeof(float);
+}
+
+template <int D>
+static cudaError_t launch_attend_d(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
+{
+    switch (c.bits_k == c.bits_v ? c.bits_k : 0) {
+    case 2: return launch_attend_b<D, 2>(c, a, ws, s);
+    case 4: return launch_attend_b<D, 4>(c, a, ws, s);
+    case 8: return launch_attend_b<D, 8>(c, a, ws, s);
+    default: return launch_attend_b<D, 0>(c, a, ws, s);
+    }
 }
 
 cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cudaStream_t s)
@@ -20,5 +32,25 @@ cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cu
     default: return launch_attend_d<256>(c, a, w, s);
     }
 }
+
+#ifdef KIVI_CHECKS
+// The first failed check of any unit; every unit's word is read and cleared.
+template <int D>
+static void check_words(int32_t& first)
+{
+    for (const int32_t w : {check_word_attend_b<D, 0>(), check_word_attend_b<D, 2>(), check_word_attend_b<D, 4>(),
+                            check_word_attend_b<D, 8>()})
+        if (first == KIVI_OK || w == KIVI_ECUDA)
+            first = w;
+}
+int32_t check_word_attend()
+{
+    int32_t first = KIVI_OK;
+    check_words<64>(first);
+    check_words<128>(first);
+    check_words<256>(first);
+    return first;
+}
+#endif
 
 }  // namespace kivi

@@ -27,84 +27,42 @@
 // in the workspace, merged by attend_combine_kernel.  The split and every
 // sum's order depend only on sizes and lengths.
 //
-// Pipeline.  Sixteen worker warps share every step; a seventeenth issues the
-// bulk copies of the packed codes and statistics into a ring of stages (one
-// stage = the keys or the values of a tile).  Per tile i the workers
-//     softmax of S(i) -> P; barrier, P(i) V(i) issued;
-//     rebuild K(i+2);       barrier, K(i+2) Q issued;      [overlaps P V]
-//     add O(i); rebuild V(i+1)                             [overlaps K Q]
-// so both products run under the workers' arithmetic.  Worker warp w reads
-// TMEM lanes 32 (w % 4) .. + 31 (tokens, later channels) and the NR/4 rows
-// w / 4 of them: a row's state (m, the factor of the last tile, its share of
-// l and o) never leaves the warps that own the row.
+// Roles.  Sixteen worker warps share every step of a tile; two copy warps bring
+// the packed codes and statistics of keys and values into rings of stages, and
+// one warp issues the products.  Per tile i the workers
+//     turn S(i) into P(i);        barrier, O(i) = V P is issued;
+//     rebuild the keys of i + 2;  barrier, S(i + 2) = K Q is issued;
+//     add O(i) to the running output and, at a row's end, store it;
+//     rebuild the values of i + 1;
+// so both products run under the workers' arithmetic.  All workers run the same
+// code at the same time on purpose: with a warpgroup per step, every step off
+// the others' critical path, the kernel was 40 % slower -- each group fetched
+// its own instruction stream once per tile, and instruction fetch, not the
+// arithmetic, set the pace.  Worker warp w reads TMEM lanes 32 (w % 4) .. + 31
+// (tokens, later channels) and the NC rows w / 4 of the tile.
 //
-// Every wait on an mbarrier gives up after two seconds: it sets the abort
+// The softmax keeps one reference maximum per row and does not move it while
+// the weights stay below 2^15.9: the exact maximum of a tile (warp reductions
+// and an exchange between the four warps of a row) is only formed when some
+// weight would pass that, which the row's first tile does and few later ones.
+//
+// Order inside 16.  A K or V operand is stored with its contiguous axis cut
+// into runs of 16 -- tokens of a key channel, channels of a value token -- and
+// element x of a run sits at position 4 (x % 4) + x / 4: the order in which
+// byte-wise extraction delivers the codes of a word, so no instruction
+// transposes them.  Tokens of a run take the same positions in V, and the
+// channel positions are undone when the output is stored.
+//
+// Every wait on an mbarrier gives up after some two seconds: it sets the abort
 // flag and records KIVI_ETIMEOUT in the workspace's status word; the CTA then
-// runs through without waiting, waits (bounded) for its copies, frees its
-// TMEM and ends.
+// runs through without waiting, waits (bounded) for its copies and products,
+// frees its TMEM and ends.
 #pragma once
 
+#include "attend_plan.h"
 #include "decode_stream.cuh"
 
 namespace kivi {
-
-constexpr int kAttTile = 128;                 // tokens per tile
-constexpr int kAttWorkers = 512;              // worker threads (16 warps)
-constexpr int kAttThreads = kAttWorkers + 32; // and the copy warp
-constexpr int kAttMaxCTAs = 160;              // workspace bound on the grid
-constexpr int kAttMaxStages = 16;
-constexpr int kAttDescs = 8;                  // tile descriptors kept in shared memory
-constexpr int kAttCutInts = 8;
-constexpr int kAttHeaderFloats = 4;
-constexpr int kAttAtom = kAttTile * 128;      // bytes of 64 channels (128 B) of a tile's tokens
-constexpr int kAttStaticSmem = 8 * 1024;      // bound on the kernel's static shared arrays
-constexpr float kAttShift = 13.0f;            // weights are scaled by 2^13
-
-// Rows per row tile for M query rows of a KV head: the next of 32, 64, 128,
-// or 32 for D = 256, whose operands leave no shared memory for more.
-inline int attend_rows(int D, int M) { return M <= 32 || D == 256 ? 32 : M <= 64 ? 64 : 128; }
-
-// Workspace: header (status word), a cut descriptor per CTA, two partial
-// (o [NR][D], m [NR], l [NR]) slots per CTA: slot 0 for a row tile that an
-// earlier CTA started, slot 1 for one that starts here and ends later.
-__host__ __device__ inline float* att_part(float* ws, int D, int NR, int cta, int slot)
-{
-    return ws + kAttHeaderFloats + kAttMaxCTAs * kAttCutInts + ((size_t)cta * 2 + slot) * NR * (D + 2);
-}
-
-template <int D, int NR>
-struct AttCfg {
-    static constexpr int NA = D / 64;                  // 64-channel atoms of a key row
-    static constexpr int NAV = D == 64 ? 2 : D / 64;   // of a value row (M = 128 spans two)
-    static constexpr int MH = D == 256 ? 2 : 1;        // 128-channel halves of the output
-    static constexpr int NC = NR / 4;                  // rows of a warp
-    static constexpr int CH = NC < 16 ? NC : 16;       // rows of one TMEM read
-    static constexpr bool STACK = NR == 32;            // both terms of P side by side in one product
-    static constexpr int PN = STACK ? 64 : NR;         // columns of the second product
-    static constexpr int PASSES = STACK ? 1 : 2;
-    static constexpr int PATOMS = STACK ? 1 : 2 * NR / 64;
-    static constexpr int QBYTES = NA * NR * 128;
-    static constexpr int O_K = 0;
-    static constexpr int O_V = O_K + NA * kAttAtom;
-    static constexpr int O_P = O_V + NAV * kAttAtom;
-    static constexpr int O_Q = O_P + PATOMS * kAttAtom;  // two buffers
-    static constexpr int O_RING = O_Q + 2 * QBYTES;
-    static constexpr int TM_S = 0;                     // TMEM columns: S(even), S(odd), O
-    static constexpr int TM_O = 2 * NR;
-    static constexpr int TM_USED = 2 * NR + MH * PN;
-    static constexpr int TM_COLS = TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
-    static constexpr int RING = kStreamSmemBytes - kAttStaticSmem - 1024 - O_RING;  // 1024: base alignment
-    static_assert(D != 256 || NR == 32, "shared memory");
-    static_assert(O_Q % 1024 == 0 && QBYTES % 1024 == 0, "operand alignment");
-};
-
-// Sizes the kernel needs besides the descriptor's.
-struct AttPlan {
-    int lgG, M, RT;       // log2 G, query rows of a KV head, row tiles
-    int ns;               // ring stages
-    int stage;            // bytes of a stage
-    int kub, vub;         // code bytes of 32 tokens: keys, values
-};
 
 // ------------------------------------------------------------------ PTX ---
 
@@ -121,20 +79,38 @@ __device__ __forceinline__ void tc_dealloc(uint32_t tm, uint32_t cols)
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// Issued by the one lane with issue != 0; the whole warp runs through, so that
+// the descriptors are computed once for the warp (uniform registers).
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t issue)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;"
+        "  @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
         : "memory");
 }
-__device__ __forceinline__ void tc_commit(uint64_t* bar)
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t issue)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{ .reg .pred q; setp.ne.u32 q, %1, 0;"
+        "  @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_addr(bar)),
+        "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r;
 }
 // N columns of this thread's TMEM lane; the values are there after tc_wait_ld,
 // which names them so that no use can be scheduled before it.
+__device__ __forceinline__ void tc_ld(float (&r)[4], uint32_t a)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                 : "r"(a));
+}
 __device__ __forceinline__ void tc_ld(float (&r)[8], uint32_t a)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -175,11 +151,51 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead)
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
-// Instruction descriptor: fp16 operands, fp32 sums, M = 128; mn: the M / N
-// axes of both operands are contiguous in shared memory.
-__host__ __device__ constexpr uint32_t mma_idesc(int n, bool mn)
+// Instruction descriptor: fp16 operands, fp32 sums, M = 128; mn_a, mn_b: the
+// M / N axis of that operand is contiguous in shared memory.
+__host__ __device__ constexpr uint32_t mma_idesc(int n, bool mn_a, bool mn_b)
 {
-    return (1u << 4) | (mn ? (1u << 15) | (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (mn_a ? 1u << 15 : 0u) | (mn_b ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+// Whether any of the warpgroup's 128 threads says so (a barrier as well).
+__device__ __forceinline__ bool group_any(int id, bool x)
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 q, %2, 0; bar.red.or.pred p, %1, 128, q; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(r)
+                 : "r"(id), "r"((uint32_t)x)
+                 : "memory");
+    return r != 0;
+}
+// Waits for the phase of parity `parity` of mbarrier b; false, with the abort
+// flag set and the timeout recorded in *status (unless null), if it has not
+// completed within kAttWaitTries attempts (some four microseconds each) or *abort
+// was set.  An iteration count and not the clock, to keep it to a few
+// instructions: every role of the kernel runs through its code once per tile,
+// so what bounds the kernel first is how much of that code the instruction
+// cache holds (inlined waits with a timer and everything unrolled to 150 KB
+// ran at a third of this speed, 44% of the instruction fetches missing).
+constexpr uint32_t kAttWaitTries = 1u << 19;
+__device__ __forceinline__ bool att_wait(uint64_t* b, uint32_t parity, int* abort, int* status)
+{
+    const uint32_t bar = smem_addr(b);
+#pragma unroll 1
+    for (uint32_t it = 0; it < kAttWaitTries; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done)
+            return true;
+        if ((it & 63u) == 63u && *(volatile int*)abort)
+            return false;
+    }
+    if (status && atomicExch(abort, 1) == 0)
+        atomicExch(status, KIVI_ETIMEOUT);
+    return false;
 }
 
 // ---------------------------------------------------------------- walker ---
@@ -217,6 +233,7 @@ __device__ __forceinline__ void att_next(AttWalk& w, const kivi_cache& c, const 
     if (++w.rr < RB)
         return;
     w.rr = 0;
+#pragma unroll 1
     while (++w.b < c.B) {
         w.s = att_seq(c, a, lgG, w.b);
         if (w.s.nt > 0)
@@ -224,26 +241,34 @@ __device__ __forceinline__ void att_next(AttWalk& w, const kivi_cache& c, const 
     }
 }
 
-// One warp: the tiles of all rows, and the position of tile `p` (any p with
-// 0 <= p < total; p is a function of the total).
-template <class F>
-__device__ __forceinline__ long long att_locate(const kivi_cache& c, const AttendArgs& a, int lgG, int RB, F p_of,
-                                                AttWalk& w)
+// One warp: the CTA's range of tiles [range[0], range[1]), the total range[2],
+// and the position of the range's first tile.
+static __device__ __noinline__ void att_locate(const kivi_cache* c, const AttendArgs* a, const AttPlan* pl,
+                                               long long* range, AttWalk* first)
 {
     const int lane = threadIdx.x & 31;
+    const long long RB = (long long)c->H * pl->RT;
     long long total = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        long long n = b0 + lane < c.B ? (long long)att_seq(c, a, lgG, b0 + lane).nt * RB : 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < c->B; b0 += 32) {
+        long long n = b0 + lane < c->B ? att_seq(*c, *a, pl->lgG, b0 + lane).nt * RB : 0;
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1)
             n += __shfl_xor_sync(0xffffffffu, n, o);
         total += n;
     }
-    const long long p = p_of(total);
+    const long long p = total * blockIdx.x / gridDim.x;
+    if (lane == 0) {
+        range[0] = p;
+        range[1] = total * (blockIdx.x + 1) / gridDim.x;
+        range[2] = total;
+    }
     long long before = 0;
-    w.b = w.rr = w.j = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const long long n = b0 + lane < c.B ? (long long)att_seq(c, a, lgG, b0 + lane).nt * RB : 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < c->B; b0 += 32) {
+        const long long n = b0 + lane < c->B ? att_seq(*c, *a, pl->lgG, b0 + lane).nt * RB : 0;
         long long inc = n;
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, inc, o);
             inc += lane >= o ? t : 0;
@@ -251,195 +276,273 @@ __device__ __forceinline__ long long att_locate(const kivi_cache& c, const Atten
         const unsigned hit = __ballot_sync(0xffffffffu, p < before + inc);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const long long at = __shfl_sync(0xffffffffu, before + inc - n, l);
-            w.b = b0 + l;
-            w.s = att_seq(c, a, lgG, w.b);
-            w.rr = (int)((p - at) / w.s.nt);
-            w.j = (int)((p - at) % w.s.nt);
-            return total;
+            if (lane == l) {
+                AttWalk w;
+                w.b = b0 + l;
+                w.s = att_seq(*c, *a, pl->lgG, w.b);
+                const long long at = p - (before + inc - n);
+                w.rr = (int)(at / w.s.nt);
+                w.j = (int)(at % w.s.nt);
+                *first = w;
+            }
+            return;
         }
         before = __shfl_sync(0xffffffffu, before + inc, 31);
     }
-    return total;
 }
 
-// What the workers need of a tile.
+// What the workers need of a tile, written by the copy warp.
 struct AttDesc {
     int b, rr, v0;            // v0: its first virtual token
     int nuq;                  // 32-token units of quantized tokens, 0 .. 4
-    int nq, Tq, res, nd;
+    int f0;                   // fp16 token (residual, then drafts) at position 0 of the tile; negative before them
+    int Tq, res, nd;
     int first, last;          // first / last tile of a row tile within this CTA's range
     int tail, mid;            // the row tile ends here / an earlier CTA started it
-    int qbuf;
     unsigned umask;           // quantized units to attend (the others' entries are skipped)
 };
 
+
 // ---------------------------------------------------------------- rebuild ---
 
-// Sixteen 2-bit codes of word w through the table x[c] = fp16(c s + z), as
-// eight half pairs of neighbouring codes.  The byte (2c) | (2c + 1) << 4 is a
-// PRMT selector of x[c] in the four-entry table: the word's codes are spread
-// to bytes, turned into selectors by one multiply-add per four codes and
-// paired by PRMT -- two instructions a code, against four and a half for
-// extracting, converting, scaling and rounding each.
-__device__ __forceinline__ void codes2_to_half(uint32_t w, float s, float z, uint32_t (&h)[8])
-{
-    const uint32_t t01 = h2_bits(__floats2half2_rn(__fmaf_rn(0.0f, s, z), __fmaf_rn(1.0f, s, z)));
-    const uint32_t t23 = h2_bits(__floats2half2_rn(__fmaf_rn(2.0f, s, z), __fmaf_rn(3.0f, s, z)));
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        q[i] = ((w >> (2 * i)) & 0x03030303u) * 0x22u + 0x10101010u;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        h[2 * b] = __byte_perm(t01, t23, __byte_perm(q[0], q[1], b | (4 + b) << 4));
-        h[2 * b + 1] = __byte_perm(t01, t23, __byte_perm(q[2], q[3], b | (4 + b) << 4));
-    }
-}
-// Code i of a byte quadruple as a float: the byte becomes the mantissa of
-// 2^23, which one exact subtraction removes.
-__device__ __forceinline__ float byte_float(uint32_t bytes, int i)
-{
-    return __fsub_rn(__uint_as_float(__byte_perm(bytes, 0x4B000000u, 0x7540 | i)), 8388608.0f);
-}
-// The codes of word w of width BITS (4 or 8) as floats, in order.
+// Position of element x of a run of 16 (its own inverse).
+__device__ __forceinline__ int run16(int x) { return (x & ~15) | (x & 3) << 2 | (x >> 2 & 3); }
+
+// Sixteen codes (BITS / 2 words) as fp16_rne(fmaf(code, s, z)), in run order:
+// h[2i] = elements i, 4 + i; h[2i + 1] = elements 8 + i, 12 + i.
+//
+// Two-bit codes go through the table x[c]: the byte (2c) | (2c + 1) << 4 is a
+// PRMT selector of x[c] among the table's four halves, so the word's codes
+// are masked to bytes, turned into selectors by one multiply-add per four
+// codes, and one PRMT per pair looks both values up: 28 instructions for 16
+// codes, against 72 that extract, convert, scale and round each.  Wider codes:
+// a byte placed in the mantissa of 2^23 by PRMT is its float plus 2^23, which
+// one exact subtraction removes.
 template <int BITS>
-__device__ __forceinline__ void codes_float(uint32_t w, float (&f)[32 / BITS])
+__device__ __forceinline__ void hat16(const uint32_t (&w)[BITS / 2], float s, float z, uint32_t (&h)[8])
 {
-    if constexpr (BITS == 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = byte_float(w, i);
-    } else {
-        const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+    if constexpr (BITS == 2) {
+        const uint32_t t01 = h2_bits(__floats2half2_rn(__fmaf_rn(0.0f, s, z), __fmaf_rn(1.0f, s, z)));
+        const uint32_t t23 = h2_bits(__floats2half2_rn(__fmaf_rn(2.0f, s, z), __fmaf_rn(3.0f, s, z)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = byte_float(e, i);
-            f[2 * i + 1] = byte_float(o, i);
+            const uint32_t q = ((w[0] >> (2 * i)) & 0x03030303u) * 0x22u + 0x10101010u;
+            h[2 * i] = __byte_perm(t01, t23, q);
+            h[2 * i + 1] = __byte_perm(t01, t23, q >> 16);
         }
-    }
-}
-
-// Keys of the stage at `st` into the operand at kb: a task is 16 tokens of two
-// neighbouring channels (one 4-byte store per token; a warp's 32 tasks cover
-// a token's 128-byte row, so the stores are free of bank conflicts).
-template <int D, int BITS>
-__device__ __forceinline__ void rebuild_keys(const uint8_t* st, uint8_t* kb, int nuq, unsigned umask, int kub)
-{
-    constexpr int P = 32 / BITS, WR = 16 / P;  // word-rows of 16 tokens
-    const float* sc = reinterpret_cast<const float*>(st + 4 * kub);
-    const float* zr = sc + 4 * D;
-#pragma unroll 1
-    for (int task = threadIdx.x; task < 4 * D; task += kAttWorkers) {
-        const int cp = task % (D / 2), hu = task / (D / 2), u = hu >> 1;
-        if (u >= nuq || !((umask >> u) & 1u))
-            continue;  // uniform over the warp
-        const float2 s = *reinterpret_cast<const float2*>(sc + u * D + 2 * cp);
-        const float2 z = *reinterpret_cast<const float2*>(zr + u * D + 2 * cp);
-        const uint2* wp = reinterpret_cast<const uint2*>(st + u * kub) + (size_t)((hu & 1) * WR) * (D / 2) + cp;
-        const int c8 = (cp & 31) >> 2;
-        uint8_t* dst = kb + (cp >> 5) * kAttAtom + hu * 16 * 128 + (cp & 3) * 4;
-        if constexpr (BITS == 2) {
-            const uint2 w = wp[0];
-            uint32_t h0[8], h1[8];
-            codes2_to_half(w.x, s.x, z.x, h0);
-            codes2_to_half(w.y, s.y, z.y, h1);
+    } else {
+        float f[16];
+        auto bytes = [&](uint32_t x, int first, int step) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                *reinterpret_cast<uint32_t*>(dst + (2 * k) * 128 + ((c8 ^ ((2 * k) & 7)) << 4)) =
-                    __byte_perm(h0[k], h1[k], 0x5410);
-                *reinterpret_cast<uint32_t*>(dst + (2 * k + 1) * 128 + ((c8 ^ ((2 * k + 1) & 7)) << 4)) =
-                    __byte_perm(h0[k], h1[k], 0x7632);
-            }
-        } else {
+            for (int b = 0; b < 4; ++b)
+                f[first + step * b] =
+                    __fsub_rn(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540 | b)), 8388608.0f);
+        };
 #pragma unroll
-            for (int r = 0; r < WR; ++r) {
-                const uint2 w = wp[(size_t)r * (D / 2)];
-                float f0[P], f1[P];
-                codes_float<BITS>(w.x, f0);
-                codes_float<BITS>(w.y, f1);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const int t = r * P + i;
-                    *reinterpret_cast<uint32_t*>(dst + t * 128 + ((c8 ^ (t & 7)) << 4)) =
-                        dequant_h2(f0[i], f1[i], s.x, z.x, s.y, z.y);
-                }
-            }
-        }
-    }
-}
-
-// Values: a task is 16 channels of one token, two 16-byte stores.  Lanes of
-// odd 64-channel columns store their second chunk first, so that the eight
-// lanes of a store phase touch eight different 16-byte columns.
-template <int D, int BITS>
-__device__ __forceinline__ void rebuild_values(const uint8_t* st, uint8_t* vb, int nuq, unsigned umask, int vub,
-                                               int lgG)
-{
-    constexpr int W = D / 16, WB = 2 * BITS;  // tasks per token, code bytes of a task
-    const int lgNG = (D == 64 ? 6 : D == 128 ? 7 : 8) - lgG;
-    const float* sc = reinterpret_cast<const float*>(st + 4 * vub);
-    const float* zr = sc + (kAttTile << lgNG);
-#pragma unroll 2
-    for (int task = threadIdx.x; task < kAttTile * W; task += kAttWorkers) {
-        const int w = task % W, t = task / W;
-        if ((t >> 5) >= nuq)
-            continue;
-        uint32_t h[8];
-        if ((umask >> (t >> 5)) & 1u) {
-            const int g = (16 * w) >> lgG;
-            const float s = sc[(t << lgNG) + g], z = zr[(t << lgNG) + g];
-            const uint8_t* src = st + (size_t)t * (D * BITS / 8) + w * WB;
-            if constexpr (BITS == 2) {
-                codes2_to_half(*reinterpret_cast<const uint32_t*>(src), s, z, h);
-            } else if constexpr (BITS == 4) {
-                const uint2 x = *reinterpret_cast<const uint2*>(src);
-                float f[8];
-                codes_float<4>(x.x, f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[k] = dequant_h2(f[2 * k], f[2 * k + 1], s, z, s, z);
-                codes_float<4>(x.y, f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[4 + k] = dequant_h2(f[2 * k], f[2 * k + 1], s, z, s, z);
+        for (int j = 0; j < BITS / 2; ++j) {
+            if constexpr (BITS == 8) {
+                bytes(w[j], 4 * j, 1);
             } else {
-                const uint4 x = *reinterpret_cast<const uint4*>(src);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[4];
-                    codes_float<8>(u4_word(x, i), f);
-                    h[2 * i] = dequant_h2(f[0], f[1], s, z, s, z);
-                    h[2 * i + 1] = dequant_h2(f[2], f[3], s, z, s, z);
-                }
+                bytes(w[j] & 0x0F0F0F0Fu, 8 * j, 2);
+                bytes((w[j] >> 4) & 0x0F0F0F0Fu, 8 * j + 1, 2);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                h[k] = 0u;  // a skipped group: its weights are 0, its values must be finite
         }
-        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-        uint8_t* row = vb + (w >> 2) * kAttAtom + t * 128;
-        const int c = 2 * (w & 3), odd = (w >> 2) & 1;
-        *reinterpret_cast<uint4*>(row + (((c + odd) ^ (t & 7)) << 4)) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (t & 7)) << 4)) = odd ? lo : hi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[2 * i] = dequant_h2(f[i], f[4 + i], s, z, s, z);
+            h[2 * i + 1] = dequant_h2(f[8 + i], f[12 + i], s, z, s, z);
+        }
+    }
+}
+
+// Words of a run of 16 codes at p, word r at p + r step.
+template <int BITS>
+__device__ __forceinline__ void run_words(const uint8_t* p, int step, uint32_t (&w)[BITS / 2])
+{
+#pragma unroll
+    for (int r = 0; r < BITS / 2; ++r)
+        w[r] = *reinterpret_cast<const uint32_t*>(p + r * step);
+}
+
+// Keys of a stage (its first nuq units): a task is 32 tokens of a channel, 64
+// contiguous bytes of the K operand, whose token axis is contiguous (rows of
+// 64 tokens per channel).  Eight neighbouring channels' stores fall in eight
+// different 16-byte columns of the swizzle.
+template <int D, int WORKERS, int BITS>
+__device__ __forceinline__ void rebuild_keys(const uint8_t* st, uint8_t* kb, int t, int su, int nuq, unsigned umask,
+                                             int kub)
+{
+    const float* sc = reinterpret_cast<const float*>(st + su * kub);
+    const float* zr = sc + su * D;
+#pragma unroll 1
+    for (int task = t; task < D * nuq; task += WORKERS) {
+        const int ch = task % D, u = task / D;
+        if (!((umask >> u) & 1u))
+            continue;  // uniform over the warp
+        const float s = sc[task], z = zr[task];
+        const uint8_t* wp = st + u * kub + ch * 4;
+        uint8_t* row = kb + ((u >> 1) * D + ch) * 128;
+        const int c0 = (u & 1) * 64, x = (ch & 7) << 4;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[BITS / 2], h[8];
+            run_words<BITS>(wp + hf * (BITS / 2) * D * 4, D * 4, w);
+            hat16<BITS>(w, s, z, h);
+            *reinterpret_cast<uint4*>(row + ((c0 + 32 * hf) ^ x)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + ((c0 + 32 * hf + 16) ^ x)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+    }
+}
+
+// Values of a stage (its first nuq units): KVW neighbouring threads rebuild the
+// token at one position, 32 channels (a statistic group, or part of one) at a
+// time, into the V operand, whose channel axis is contiguous (rows of 64
+// channels per token).
+template <int D, int WORKERS, int BITS>
+__device__ __forceinline__ void rebuild_values(const uint8_t* st, uint8_t* vb, int x, int su, int nuq, unsigned umask,
+                                               int vub, int lgG)
+{
+    const int lgT = (WORKERS == 512 ? 2 : 1) + (su == 2 ? 1 : 0);  // threads per token
+    const int t = x >> lgT;
+    if ((t >> 5) >= nuq)
+        return;
+    const int tok = run16(t), lgNG = (D == 64 ? 6 : D == 128 ? 7 : 8) - lgG;
+    const bool live = (umask >> (t >> 5)) & 1u;
+    const float* sc = reinterpret_cast<const float*>(st + su * vub) + (tok << lgNG);
+    const float* zr = sc + (32 * su << lgNG);
+    const uint8_t* src = st + tok * (D * BITS / 8);
+    uint8_t* row = vb + t * 128;
+    const int sw = (t & 7) << 4;
+#pragma unroll 1
+    for (int c = 32 * (x & ((1 << lgT) - 1)); c < D; c += 32 << lgT) {
+        const float s = sc[c >> lgG], z = zr[c >> lgG];
+        uint8_t* dst = row + (c >> 6) * (kAttTile * 128);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[BITS / 2], h[8];
+            run_words<BITS>(src + (c + 16 * hf) * BITS / 8, 4, w);
+            hat16<BITS>(w, s, z, h);
+            if (!live) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    h[k] = 0u;  // a skipped group: its weights are 0, its values must be finite
+            }
+            const int c0 = (c & 32) * 2 + 32 * hf;
+            *reinterpret_cast<uint4*>(dst + (c0 ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + ((c0 + 16) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
     }
 }
 
 // ----------------------------------------------------------------- kernel ---
 
-template <int D, int NR>
-__global__ void __launch_bounds__(kAttThreads, 1)
-attend_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, float* __restrict__ ws)
+// ------------------------------------------------------------- cold paths ---
+// Out of line, so that a worker's loop over whole quantized tiles stays small
+// and contiguous: instruction fetch is what bounds it first.
+
+// Q of a new row tile, rows beyond the problem's zero.
+template <int D, int NR, int WORKERS>
+static __device__ __noinline__ void att_load_q(const kivi_cache* c, const AttendArgs* a, const AttPlan* pl,
+                                               const AttDesc* d, uint8_t* qs, int t)
+{
+    const int h = d->rr / pl->RT, rt = d->rr - h * pl->RT;
+    const uint4* q =
+        reinterpret_cast<const uint4*>(a->q + ((size_t)d->b * a->Hq + (size_t)h * (a->Hq / c->H)) * a->N * D);
+#pragma unroll 1
+    for (int x = t; x < NR * D / 8; x += WORKERS) {
+        const int ch = x % (D / 8), r = x / (D / 8), row = rt * NR + r;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row < pl->M && (!a->k || row % a->N < d->nd))
+            v = ldg_checked(q + (size_t)row * (D / 8) + ch);
+        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+    }
+}
+
+// Which drafts any row attends, into seen[4]; every worker calls it.
+template <int WORKERS>
+static __device__ __noinline__ void att_seen(const AttendArgs* a, const AttDesc* d, unsigned long long* seen, int t)
+{
+    const int W = (a->N + 63) >> 6;
+    if (t < 4)
+        seen[t] = 0ull;
+    named_bar(2, WORKERS);
+#pragma unroll 1
+    for (int x = t; x < d->nd * W; x += WORKERS)
+        atomicOr(&seen[x % W],
+                 (unsigned long long)ldg_checked(a->mask + ((size_t)d->b * a->N + x / W) * W + x % W));
+    named_bar(2, WORKERS);
+}
+
+// The fp16 tokens (residual, then drafts) of a tile into the K (which = 0) or V
+// operand; zero where no row attends one.  A thread takes D / GROUPS channels
+// of a token: an element of each channel's row of K, run order in V.
+template <int D, int GROUPS>
+static __device__ __noinline__ void att_fp16_rows(const kivi_cache* c, const AttendArgs* a, const AttPlan* pl,
+                                                  const AttDesc* d, const unsigned long long* seen, uint8_t* dst,
+                                                  int which, int t)
+{
+    const int e = which == 0 ? t & 127 : t / GROUPS, part = which == 0 ? t >> 7 : t % GROUPS;
+    if (e < 32 * d->nuq)
+        return;
+    const int f = d->f0 + e, j = f - d->res, RG = c->R + c->G;
+    const size_t bh = (size_t)d->b * c->H + d->rr / pl->RT;
+    const uint16_t* src = nullptr;
+    if (j < 0) {
+        int s = d->Tq % RG + f;
+        s = s >= RG ? s - RG : s;
+        src = (which == 0 ? c->kres : c->vres) + (bh * RG + s) * D;
+    } else if (j < d->nd && (seen[j >> 6] >> (j & 63)) & 1) {
+        src = (which == 0 ? a->k : a->v) + (bh * a->N + j) * D;
+    }
+    uint8_t* kd = dst + (e >> 6) * D * 128 + (e & 7) * 2;
+    uint8_t* vd = dst + e * 128;
+    const int kx = ((e >> 3) & 7) << 4, vx = (e & 7) << 4;
+#pragma unroll 1
+    for (int c0 = part * (D / GROUPS); c0 < (part + 1) * (D / GROUPS); c0 += 16) {
+        uint4 y = make_uint4(0u, 0u, 0u, 0u), z = y;
+        if (src) {
+            y = ldg_checked(reinterpret_cast<const uint4*>(src + c0));
+            z = ldg_checked(reinterpret_cast<const uint4*>(src + c0) + 1);
+        }
+        if (which == 0) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                *reinterpret_cast<uint16_t*>(kd + (c0 + k) * 128 + (kx ^ ((k & 7) << 4))) = u4_half(k < 8 ? y : z, k & 7);
+        } else {
+            const uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int sel = k & 1 ? 0x7632 : 0x5410;
+                o[2 * k] = __byte_perm(q[k >> 1], q[2 + (k >> 1)], sel);
+                o[2 * k + 1] = __byte_perm(q[4 + (k >> 1)], q[6 + (k >> 1)], sel);
+            }
+            uint8_t* run = vd + (c0 >> 6) * (kAttTile * 128);
+            const int cc = (c0 & 63) * 2;
+            *reinterpret_cast<uint4*>(run + (cc ^ vx)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(run + ((cc + 16) ^ vx)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// B: the codes' width if keys and values have the same (it then is a constant
+// of the kernel, and its loops hold no other width's code), else 0.
+template <int D, int NR, int B>
+__global__ void __launch_bounds__(AttCfg<D, NR>::THREADS, AttCfg<D, NR>::CTAS)
+attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ AttendArgs a,
+              const __grid_constant__ AttPlan pl, float* __restrict__ ws)
 {
     using C = AttCfg<D, NR>;
     constexpr int NC = C::NC, CH = C::CH, MH = C::MH;
+    constexpr int kCopyWarp = C::WORKERS / 32, kMmaWarp = kCopyWarp + 2;
     extern __shared__ uint8_t att_smem[];
     __shared__ AttDesc s_desc[kAttDescs];
-    __shared__ unsigned long long s_seen[4][4];   // drafts any row attends, by tile and word
-    __shared__ __align__(16) float s_red[2][4][NC][4];  // maxima, sums: [row group][row][lane quadrant]
-    __shared__ uint64_t s_full[kAttMaxStages], s_empty[kAttMaxStages], s_sbar[2], s_obar;
-    __shared__ unsigned s_umask[kAttMaxStages];
+    __shared__ unsigned long long s_seen[4][4];                // drafts any row attends, by tile
+    __shared__ __align__(16) float s_red[C::GROUPS][NC][4];            // maxima: [row group][row][lane quadrant]
+    __shared__ float s_part[C::GROUPS][128];
+    __shared__ __align__(16) float s_ref[C::GROUPS][C::REG_REF ? 1 : NC];
+    __shared__ uint64_t s_full[2][kAttMaxStages], s_empty[2][kAttMaxStages];
+    __shared__ uint64_t s_sdone[2], s_odone;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_never;
     __shared__ AttWalk s_walk;
@@ -450,33 +553,29 @@ attend_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, float* _
     int* status = reinterpret_cast<int*>(ws);
     const long long ctas = gridDim.x, cta = blockIdx.x;
 
-    if (warp == 0) {
-        AttWalk w;
-        long long p0 = 0;
-        const long long total = att_locate(c, a, pl.lgG, RB, [&](long long t) { return p0 = t * cta / ctas; }, w);
+    if (warp == kCopyWarp) {
+        att_locate(&c, &a, &pl, s_range, &s_walk);
+    } else if (warp == kMmaWarp) {
+        tc_alloc(&s_tmem, C::TM_COLS);
         if (lane == 0) {
-            s_range[0] = p0;
-            s_range[1] = total * (cta + 1) / ctas;
-            s_range[2] = total;
-            s_walk = w;
             s_abort = s_never = 0;
             if (cta == 0)
                 *status = KIVI_OK;
             for (int i = 0; i < pl.ns; ++i) {
-                mbar_init(&s_full[i], 1);
-                mbar_init(&s_empty[i], kAttWorkers / 32);
+                for (int x = 0; x < 2; ++x) {
+                    mbar_init(&s_full[x][i], 1);
+                    mbar_init(&s_empty[x][i], C::WORKERS / 32);
+                }
             }
-            mbar_init(&s_sbar[0], 1);
-            mbar_init(&s_sbar[1], 1);
-            mbar_init(&s_obar, 1);
+            mbar_init(&s_sdone[0], 1);
+            mbar_init(&s_sdone[1], 1);
+            mbar_init(&s_odone, 1);
             mbar_fence_init();
         }
-    } else if (warp == 1) {
-        tc_alloc(&s_tmem, C::TM_COLS);
     }
     if constexpr (D == 64) {  // the second 64 rows of V^T are not channels: zero
-        for (int i = tid; i < kAttAtom / 16; i += kAttThreads)
-            reinterpret_cast<uint4*>(sm + C::O_V + kAttAtom)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = tid; i < C::VATOM / 16; i += C::THREADS)
+            reinterpret_cast<uint4*>(sm + C::O_V + C::VATOM)[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
     }
     tc_fence_before();
@@ -484,485 +583,500 @@ attend_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, float* _
     tc_fence_after();
     const uint32_t tm = s_tmem;
     const int n = (int)(s_range[1] - s_range[0]);
-    int* cut = reinterpret_cast<int*>(ws + kAttHeaderFloats) + (size_t)cta * kAttCutInts;
-    if (tid == 0)
-        cut[0] = 0;
+    auto wait = [&](uint64_t* bar, int phase) { return att_wait(bar, phase & 1, &s_abort, status); };
 
-    if (warp == kAttWorkers / 32) {
-        // ------------------------------------------------------ copies ---
-        // in the order the workers consume: K0, K1, V0, K2, V1, ...
-        AttWalk w[2] = {s_walk, s_walk};  // next tile whose keys / values are copied
-        int at[2] = {0, 0};
-        int sp = 0;
-        uint8_t* ring = sm + C::O_RING;
-        while (at[1] < n) {
-            const int which = at[0] < n && at[0] < at[1] + 2 ? 0 : 1;
-            AttWalk& x = w[which];
-            const int v0 = x.j * kAttTile;
-            const int nuq = min(max((x.s.nq - v0) >> 5, 0), 4);
-            if (nuq > 0) {
-                const int slot = sp % pl.ns, round = sp / pl.ns;
-                bool ok = true;
-                if (round > 0)
-                    ok = mbar_wait_bounded(&s_empty[slot], (round - 1) & 1, &s_abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    if (lane == 0 && atomicExch(&s_abort, 1) == 0)
-                        atomicExch(status, KIVI_ETIMEOUT);
-                    break;
-                }
-                const size_t bh = (size_t)x.b * c.H + x.rr / pl.RT;
-                const int v = v0 + 32 * lane;  // this lane's unit
-                int t0 = v;
-                bool go = lane < nuq;
-                if (go && a.blocks) {
-                    const int g = ldg_checked(a.blocks + bh * a.n_keep + (v >> pl.lgG));
-                    go = g >= 0 && g < x.s.Tq >> pl.lgG;
-                    t0 = (g << pl.lgG) + (v & (c.G - 1));
-                }
-                const unsigned mask = __ballot_sync(0xffffffffu, go);
-                const uint32_t stat = which == 0 ? D * 4 : 32 * (D >> pl.lgG) * 4;
-                const uint32_t code = which == 0 ? pl.kub : pl.vub;
-                if (lane == 0) {
-                    s_umask[slot] = mask;
-                    mbar_arrive_tx(&s_full[slot], __popc(mask) * (code + 2 * stat));
-                }
-                __syncwarp();
-                if (go) {
-                    const uint8_t* src;
-                    const float *ss, *zz;
-                    if (which == 0) {
-                        const int P = 32 / c.bits_k;
-                        src = reinterpret_cast<const uint8_t*>(c.kq + (bh * (c.Tmax / P) + t0 / P) * D);
-                        const size_t so = (bh * (c.Tmax >> pl.lgG) + (t0 >> pl.lgG)) * D;
-                        ss = c.kscale + so;
-                        zz = c.kzero + so;
-                    } else {
-                        src = reinterpret_cast<const uint8_t*>(c.vq) + (bh * c.Tmax + t0) * (D * c.bits_v / 8);
-                        const size_t so = (bh * c.Tmax + t0) * (D >> pl.lgG);
-                        ss = c.vscale + so;
-                        zz = c.vzero + so;
-                    }
-                    uint8_t* d = ring + (size_t)slot * pl.stage;
-                    if (KIVI_IN_RANGE(src, code) && KIVI_IN_RANGE(ss, stat) && KIVI_IN_RANGE(zz, stat)) {
-                        bulk_g2s(d + lane * code, src, code, &s_full[slot]);
-                        bulk_g2s(d + 4 * code + lane * stat, ss, stat, &s_full[slot]);
-                        bulk_g2s(d + 4 * code + 4 * stat + lane * stat, zz, stat, &s_full[slot]);
-                    }
-                }
-                ++sp;
-            }
-            ++at[which];
-            att_next(x, c, a, pl.lgG, RB);
+    if (warp >= kCopyWarp && warp < kMmaWarp) {
+        // ---------------------------------------------------------- copy ---
+        const int which = warp - kCopyWarp;  // 0: keys, 1: values
+        AttWalk w = s_walk;
+        const bool starts_mid = w.j > 0;
+        const int b0 = w.b, rr0 = w.rr;
+        int* cut = reinterpret_cast<int*>(ws + kAttHeaderFloats) + (size_t)cta * kAttCutInts;
+        if (warp == kCopyWarp && lane == 0) {
+            cut[0] = 0;
+            cut[4] = n;
         }
-        // every copy has landed before the CTA may end (the workers have
+        // a unit: 32 tokens' codes, then its scales, then its zeros, at these
+        // byte strides per 32 tokens (keys: statistics per group)
+        const uint32_t code = which == 0 ? pl.kub : pl.vub;
+        const uint32_t stat = which == 0 ? D * 4 : 32 * (D >> pl.lgG) * 4;
+        const uint8_t* codes = reinterpret_cast<const uint8_t*>(which == 0 ? c.kq : c.vq);
+        const uint8_t* scales = reinterpret_cast<const uint8_t*>(which == 0 ? c.kscale : c.vscale);
+        const uint8_t* zeros = reinterpret_cast<const uint8_t*>(which == 0 ? c.kzero : c.vzero);
+        const int lgs = which == 0 ? pl.lgG : 5;  // tokens of a statistic unit
+        uint8_t* ring = sm + C::O_RING + (which == 0 ? 0 : pl.ns * pl.kst);
+        const int stage = which == 0 ? pl.kst : pl.vst;
+        int slot = 0, round = 0, sent = 0;
+        bool alive = true;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int v0 = w.j * kAttTile;
+            const int nuq = min(max((w.s.nq - v0) >> 5, 0), 4);
+            const size_t bh = (size_t)w.b * c.H + w.rr / pl.RT;
+            const int v = v0 + 32 * lane;  // this lane's unit of 32 tokens
+            int t0 = v;
+            bool go = lane < nuq;
+            if (go && a.blocks) {
+                const int g = ldg_checked(a.blocks + bh * a.n_keep + (v >> pl.lgG));
+                go = g >= 0 && g < w.s.Tq >> pl.lgG;
+                t0 = (g << pl.lgG) + (v & (c.G - 1));
+            }
+            const unsigned mask = __ballot_sync(0xffffffffu, go);
+#pragma unroll 1
+            for (int u0 = 0; u0 < 4; u0 += pl.su) {
+            if (round > 0 && !__all_sync(0xffffffffu, wait(&s_empty[which][slot], round - 1))) {
+                alive = false;
+                break;
+            }
+            uint64_t* bar = &s_full[which][slot];
+            const unsigned pmask = mask >> u0 & ((1u << pl.su) - 1);
+            if (lane == 0) {
+                if (which == 0 && u0 == 0) {
+                AttDesc& d = s_desc[i & (kAttDescs - 1)];
+                d.b = w.b;
+                d.rr = w.rr;
+                d.v0 = v0;
+                d.nuq = nuq;
+                d.f0 = v0 - w.s.nq;
+                d.Tq = w.s.Tq;
+                d.res = w.s.len - w.s.Tq;
+                d.nd = w.s.nd;
+                d.tail = w.j == w.s.nt - 1;
+                d.mid = starts_mid && w.b == b0 && w.rr == rr0;
+                d.first = w.j == 0 || i == 0;
+                d.last = d.tail || i == n - 1;
+                d.umask = mask;
+                if (__builtin_expect(i == n - 1 && !d.tail && !d.mid, 0)) {
+                    // the row tile starts in this range and ends in a later one, at tile `end`
+                    const long long end = s_range[1] + (w.s.nt - 1 - w.j);
+                    int k = (int)cta + 1;
+#pragma unroll 1
+                    while (s_range[2] * (k + 1) / ctas < end)
+                        ++k;
+                    cut[1] = w.b;
+                    cut[2] = w.rr;
+                    cut[3] = k;
+                    cut[0] = 1;
+                }
+                }
+                mbar_arrive_tx(bar, __popc(pmask) * (code + 2 * stat));
+            }
+            __syncwarp();
+            const int u = lane - u0;  // unit of the stage
+            if (go && u >= 0 && u < pl.su) {
+                const uint8_t* src = codes + (bh * (c.Tmax >> 5) + (t0 >> 5)) * code;
+                const size_t so = (bh * (c.Tmax >> lgs) + (t0 >> lgs)) * stat;
+                uint8_t* d = ring + slot * stage;
+                if (KIVI_IN_RANGE(src, code) && KIVI_IN_RANGE(scales + so, stat) && KIVI_IN_RANGE(zeros + so, stat)) {
+                    bulk_g2s(d + u * code, src, code, bar);
+                    bulk_g2s(d + pl.su * code + u * stat, scales + so, stat, bar);
+                    bulk_g2s(d + pl.su * (code + stat) + u * stat, zeros + so, stat, bar);
+                }
+            }
+            ++sent;
+            if (++slot == pl.ns) {
+                slot = 0;
+                ++round;
+            }
+            }
+            if (!alive)
+                break;
+            att_next(w, c, a, pl.lgG, RB);
+        }
+        // every copy has landed before the CTA may end (the groups have
         // consumed them all unless a wait gave up)
-        for (int s = max(0, sp - pl.ns); s < sp; ++s)
-            mbar_wait_bounded(&s_full[s % pl.ns], (s / pl.ns) & 1, &s_never);
-    } else if (n > 0) {
-        // ----------------------------------------------------- workers ---
-        const int qd = warp & 3, wg = warp >> 2;
+#pragma unroll 1
+        for (int s = max(0, sent - pl.ns); s < sent; ++s)
+            att_wait(&s_full[which][s % pl.ns], (s / pl.ns) & 1, &s_never, nullptr);
+    } else if (warp == kMmaWarp) {
+        // ----------------------------------------------------------- MMA ---
+        const uint32_t one = elect_lane();
+        const uint64_t kd = smem_desc(smem_addr(sm + C::O_K), D * 128);
+        const uint64_t qd = smem_desc(smem_addr(sm + C::O_Q), 16);
+        const uint64_t vd = smem_desc(smem_addr(sm + C::O_V), C::VATOM);
+        const uint64_t pd = smem_desc(smem_addr(sm + C::O_P), C::PATOM);
+        // S(0), S(1), then O(i) and S(i + 2)
+        auto scores = [&](int i) {
+            named_bar(1, C::WORKERS + 32);
+            tc_fence_after();
+            const uint32_t dst = tm + C::TM_S + (i & 1) * NR;
+#pragma unroll 1
+            for (int a64 = 0; a64 < D / 64; ++a64)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma(dst, kd + ((a64 * 4 + k) * 2048 >> 4), qd + ((a64 * (NR * 128) + k * 32) >> 4),
+                           mma_idesc(NR, true, false), a64 + k > 0, one);
+            tc_commit(&s_sdone[i & 1], one);
+        };
+#pragma unroll 1
+        for (int i = -2; i < n; ++i) {
+            if (i >= 0) {  // O(i)
+                named_bar(1, C::WORKERS + 32);
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < MH * C::PASSES; ++x) {
+                    const int h = x / C::PASSES, pass = x % C::PASSES;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma(tm + C::TM_O + h * C::PN, vd + ((h * 2 * C::VATOM + k * 2048) >> 4),
+                               pd + ((pass * C::PTERM + k * 2048) >> 4), mma_idesc(C::PN, true, true), pass + k > 0, one);
+                }
+                tc_commit(&s_odone, one);
+            }
+            if (i + 2 < n)
+                scores(i + 2);
+        }
+        // every product has ended before the TMEM is freed
+        if (n > 0) {
+            att_wait(&s_sdone[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_never, nullptr);
+            att_wait(&s_odone, (n - 1) & 1, &s_never, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- workers ---
+        const int qd = warp & 3, wg = warp >> 2, t = tid;
         const uint32_t lanes = (uint32_t)(qd * 32) << 16;
         const float sl2 = a.sm_scale * 1.4426950408889634f;
-        const int RG = c.R + c.G;
-        int sc = 0;                        // stages consumed
-        float m = -INFINITY, alpha = 1.0f; // of row wg NC + lane, lane < NC
-        float l[NC], o[MH][NC];
+        const int W = (a.N + 63) >> 6;
+        int slot[2] = {0, 0}, round[2] = {0, 0};  // of the key and the value ring
 
-        auto wait = [&](uint64_t* bar, int phase) {
-            if (!mbar_wait_bounded(bar, phase & 1, &s_abort))
-                if (atomicExch(&s_abort, 1) == 0)
-                    atomicExch(status, KIVI_ETIMEOUT);
-        };
-        auto barrier = [&]() { named_bar(1, kAttWorkers); };
-
-        // tile descriptors, written by thread 0 two tiles before their first use
-        AttWalk dw = s_walk;
-        int dn = 0, dq = 0;
-        auto describe = [&]() {
-            if (dn >= n)
-                return;
-            AttDesc& d = s_desc[dn & (kAttDescs - 1)];
-            const int v0 = dw.j * kAttTile;
-            d.b = dw.b;
-            d.rr = dw.rr;
-            d.v0 = v0;
-            d.nuq = min(max((dw.s.nq - v0) >> 5, 0), 4);
-            d.nq = dw.s.nq;
-            d.Tq = dw.s.Tq;
-            d.res = dw.s.len - dw.s.Tq;
-            d.nd = dw.s.nd;
-            d.tail = dw.j == dw.s.nt - 1;
-            d.mid = s_walk.j > 0 && dw.b == s_walk.b && dw.rr == s_walk.rr;
-            d.first = dw.j == 0 || dn == 0;
-            d.last = d.tail || dn == n - 1;
-            if (d.first)
-                dq ^= 1;
-            d.qbuf = dq;
-            if (dn == n - 1 && !d.tail && !d.mid) {
-                // the row starts in this range and ends in a later one
-                const long long end = s_range[1] + (dw.s.nt - 1 - dw.j);
-                int k = (int)cta + 1;
-                while (s_range[2] * (k + 1) / ctas < end)
-                    ++k;
-                cut[1] = dw.b;
-                cut[2] = dw.rr;
-                cut[3] = k;
-                cut[4] = (int)(s_range[2] & 0x7fffffff);
-                cut[5] = (int)(s_range[2] >> 31);
-                cut[0] = 1;
-            }
-            ++dn;
-            att_next(dw, c, a, pl.lgG, RB);
-        };
-
-        // fp16 rows of a tile (residual and drafts) into an operand buffer
-        auto copy_rows = [&](const AttDesc& d, int ti, const uint16_t* ringp, const uint16_t* draft, uint8_t* dst) {
-            const int e0 = 32 * d.nuq, NCH = D / 8;
-            const size_t bh = (size_t)d.b * c.H + d.rr / pl.RT;
-            const int s0 = d.Tq % RG;
-#pragma unroll 4
-            for (int i = tid; i < (kAttTile - e0) * NCH; i += kAttWorkers) {
-                const int ch = i % NCH, e = e0 + i / NCH;
-                const int f = d.v0 + e - d.nq;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (f < d.res) {
-                    const int slot = s0 + f >= RG ? s0 + f - RG : s0 + f;
-                    x = ldg_checked(reinterpret_cast<const uint4*>(ringp + (bh * RG + slot) * D) + ch);
-                } else {
-                    const int j = f - d.res;
-                    if (j < d.nd && (s_seen[ti & 3][j >> 6] >> (j & 63)) & 1)
-                        x = ldg_checked(reinterpret_cast<const uint4*>(draft + (bh * a.N + j) * D) + ch);
-                }
-                *reinterpret_cast<uint4*>(dst + (ch >> 3) * kAttAtom + e * 128 + (((ch & 7) ^ (e & 7)) << 4)) = x;
+        auto release = [&](int which) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s_empty[which][slot[which]]);
+            if (++slot[which] == pl.ns) {
+                slot[which] = 0;
+                ++round[which];
             }
         };
-
-        // K operand (and a new row tile's Q) of tile i
         auto keys = [&](int i) {
-            AttDesc& d = s_desc[i & (kAttDescs - 1)];
-            const int h = d.rr / pl.RT, rt = d.rr - h * pl.RT;
-            const int gq = a.Hq / c.H;
-            const bool drafts = d.nd > 0 && d.v0 + kAttTile > d.nq + d.res;
-            if (drafts) {  // which drafts any row attends
-                if (tid < 4)
-                    s_seen[i & 3][tid] = 0ull;
-                barrier();
-                const int W = (a.N + 63) >> 6;
-                for (int x = tid; x < d.nd * W; x += kAttWorkers)
-                    atomicOr(&s_seen[i & 3][x % W],
-                             (unsigned long long)ldg_checked(a.mask + ((size_t)d.b * a.N + x / W) * W + x % W));
-                barrier();
-            }
-            if (d.first) {
-                uint8_t* qb = sm + C::O_Q + d.qbuf * C::QBYTES;
-                constexpr int NCH = D / 8;
-#pragma unroll 2
-                for (int x = tid; x < NR * NCH; x += kAttWorkers) {
-                    const int ch = x % NCH, r = x / NCH, row = rt * NR + r;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < pl.M && (!a.k || row % a.N < d.nd))
-                        v = ldg_checked(reinterpret_cast<const uint4*>(
-                                            a.q + (((size_t)d.b * a.Hq + (size_t)h * gq) * a.N + row) * D) + ch);
-                    *reinterpret_cast<uint4*>(qb + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+            const AttDesc& d = s_desc[i & (kAttDescs - 1)];
+#pragma unroll 1
+            for (int u0 = 0; u0 < 4; u0 += pl.su) {
+                wait(&s_full[0][slot[0]], round[0]);  // (the first stage brings the tile's descriptor)
+                const uint8_t* st = sm + C::O_RING + slot[0] * pl.kst;
+                uint8_t* kb = sm + C::O_K + u0 * D * 64;
+                const int nu = min(d.nuq - u0, pl.su);
+                const unsigned um = d.umask >> u0;
+                switch (B ? B : c.bits_k) {
+                case 2: rebuild_keys<D, C::WORKERS, B ? B : 2>(st, kb, t, pl.su, nu, um, pl.kub); break;
+                case 4: rebuild_keys<D, C::WORKERS, B ? B : 4>(st, kb, t, pl.su, nu, um, pl.kub); break;
+                default: rebuild_keys<D, C::WORKERS, B ? B : 8>(st, kb, t, pl.su, nu, um, pl.kub); break;
                 }
+                release(0);
             }
-            if (d.nuq > 0) {
-                const int slot = sc % pl.ns;
-                wait(&s_full[slot], sc / pl.ns);
-                const unsigned um = s_umask[slot];
-                if (tid == 0)
-                    d.umask = um;
-                const uint8_t* st = sm + C::O_RING + (size_t)slot * pl.stage;
-                switch (c.bits_k) {
-                case 2: rebuild_keys<D, 2>(st, sm + C::O_K, d.nuq, um, pl.kub); break;
-                case 4: rebuild_keys<D, 4>(st, sm + C::O_K, d.nuq, um, pl.kub); break;
-                default: rebuild_keys<D, 8>(st, sm + C::O_K, d.nuq, um, pl.kub); break;
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&s_empty[slot]);
-                ++sc;
+            if (__builtin_expect(d.first, 0))
+                att_load_q<D, NR, C::WORKERS>(&c, &a, &pl, &d, sm + C::O_Q, t);
+            if (__builtin_expect(d.nuq < 4, 0)) {
+                if (d.nd > 0 && d.f0 + kAttTile > d.res)
+                    att_seen<C::WORKERS>(&a, &d, s_seen[i & 3], t);
+                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], sm + C::O_K, 0, t);
             }
-            if (d.nuq < 4)
-                copy_rows(d, i, c.kres, a.k, sm + C::O_K);
         };
         auto values = [&](int i) {
             const AttDesc& d = s_desc[i & (kAttDescs - 1)];
-            if (d.nuq > 0) {
-                const int slot = sc % pl.ns;
-                wait(&s_full[slot], sc / pl.ns);
-                const uint8_t* st = sm + C::O_RING + (size_t)slot * pl.stage;
-                switch (c.bits_v) {
-                case 2: rebuild_values<D, 2>(st, sm + C::O_V, d.nuq, s_umask[slot], pl.vub, pl.lgG); break;
-                case 4: rebuild_values<D, 4>(st, sm + C::O_V, d.nuq, s_umask[slot], pl.vub, pl.lgG); break;
-                default: rebuild_values<D, 8>(st, sm + C::O_V, d.nuq, s_umask[slot], pl.vub, pl.lgG); break;
+#pragma unroll 1
+            for (int u0 = 0; u0 < 4; u0 += pl.su) {
+                wait(&s_full[1][slot[1]], round[1]);
+                const uint8_t* st = sm + C::O_RING + pl.ns * pl.kst + slot[1] * pl.vst;
+                uint8_t* vb = sm + C::O_V + u0 * 32 * 128;
+                const int nu = min(d.nuq - u0, pl.su);
+                const unsigned um = d.umask >> u0;
+                switch (B ? B : c.bits_v) {
+                case 2: rebuild_values<D, C::WORKERS, B ? B : 2>(st, vb, t, pl.su, nu, um, pl.vub, pl.lgG); break;
+                case 4: rebuild_values<D, C::WORKERS, B ? B : 4>(st, vb, t, pl.su, nu, um, pl.vub, pl.lgG); break;
+                default: rebuild_values<D, C::WORKERS, B ? B : 8>(st, vb, t, pl.su, nu, um, pl.vub, pl.lgG); break;
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&s_empty[slot]);
-                ++sc;
+                release(1);
             }
-            if (d.nuq < 4)
-                copy_rows(d, i, c.vres, a.v, sm + C::O_V);
+            if (__builtin_expect(d.nuq < 4, 0))
+                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], sm + C::O_V, 1, t);
         };
-        auto publish = [&]() {  // operands in shared memory, TMEM reads done
+        auto publish = [&]() {  // operands in shared memory, TMEM reads done: the MMA warp goes on
             fence_async_smem();
             tc_fence_before();
-            barrier();
-        };
-        auto issue_s = [&](int i) {
-            if (tid != 0)
-                return;
-            tc_fence_after();
-            const uint32_t kb = smem_addr(sm + C::O_K);
-            const uint32_t qb = smem_addr(sm + C::O_Q + s_desc[i & (kAttDescs - 1)].qbuf * C::QBYTES);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                tc_mma(tm + C::TM_S + (i & 1) * NR, smem_desc(kb + (k >> 2) * kAttAtom + (k & 3) * 32, 16),
-                       smem_desc(qb + (k >> 2) * (NR * 128) + (k & 3) * 32, 16), mma_idesc(NR, false), k > 0);
-            tc_commit(&s_sbar[i & 1]);
-        };
-        auto issue_o = [&]() {
-            if (tid != 0)
-                return;
-            tc_fence_after();
-            const uint32_t vb = smem_addr(sm + C::O_V), pb = smem_addr(sm + C::O_P);
-#pragma unroll
-            for (int h = 0; h < MH; ++h)
-#pragma unroll
-                for (int x = 0; x < C::PASSES * (kAttTile / 16); ++x) {
-                    const int pass = x / (kAttTile / 16), k = x % (kAttTile / 16);
-                    tc_mma(tm + C::TM_O + h * C::PN, smem_desc(vb + h * 2 * kAttAtom + k * 2048, kAttAtom),
-                           smem_desc(pb + pass * (C::PATOMS / 2) * kAttAtom + k * 2048, kAttAtom),
-                           mma_idesc(C::PN, true), x > 0);
-                }
-            tc_commit(&s_obar);
+            named_bar(1, C::WORKERS + 32);
         };
 
-        // P of tile i
-        auto softmax = [&](int i) {
-            const AttDesc& d = s_desc[i & (kAttDescs - 1)];
-            const int rt = d.rr % pl.RT;
-            if (d.first) {
-                m = -INFINITY;
+        // A row's weights are 2^(S sl2 - ref); -inf before its first token.  All
+        // threads of a row hold its reference: in registers up to 16 rows, in
+        // shared memory beyond.
+        float ref[C::REG_REF ? NC : 1];
+        float l[NC], o[MH][NC];
+        auto my_ref = [&]() {  // of row `lane`
+            float x = -INFINITY;
+            if constexpr (C::REG_REF) {
 #pragma unroll
                 for (int k = 0; k < NC; ++k)
-                    l[k] = 0.0f;
+                    x = lane == k ? ref[k] : x;
+            } else {
+                x = s_ref[wg][lane % NC];
             }
-            // tokens of this warp's lanes: a quantized unit, or fp16 tokens
+            return x;
+        };
+
+        // the row tile that ends with tile i: its output, or a piece of it
+        auto finish = [&](int i) {
+            const AttDesc& d = s_desc[i & (kAttDescs - 1)];
+            // sums of the weights over the 128 tokens, through P's buffer (its
+            // product is done): each thread's row of NC, then 128 / NC partial
+            // sums a row
+            const int x = tid & 127;
+            float* own = reinterpret_cast<float*>(sm + C::O_P) + (wg * 128 + x) * NC;
+#pragma unroll
+            for (int k = 0; k < NC; k += 4)
+                *reinterpret_cast<float4*>(own + k) = make_float4(l[k], l[k + 1], l[k + 2], l[k + 3]);
+            named_bar(3 + wg, 128);
+            const float* col = reinterpret_cast<float*>(sm + C::O_P) + (wg * 128 + x / NC * NC) * NC + x % NC;
+            float part = 0.0f;
+#pragma unroll 4
+            for (int k = 0; k < NC; ++k)
+                part += col[k * NC];
+            s_part[wg][x] = part;
+            named_bar(3 + wg, 128);
+            float L = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 128; k += NC)
+                L += s_part[wg][k + lane % NC];
+            const int h = d.rr / pl.RT, r0 = (d.rr - h * pl.RT) * NR + wg * NC;
+            float *dst, scale = 1.0f;
+            bool mine = lane < NC;  // row `lane` is stored
+            if (d.tail && !d.mid) {
+                scale = L > 0.0f ? 1.0f / L : 0.0f;
+                mine = mine && r0 + lane < pl.M && (!a.k || (r0 + lane) % a.N < d.nd);
+                dst = a.out + (((size_t)d.b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + r0) * D;
+            } else {
+                float* piece = att_part(ws, D, NR, (int)cta, d.mid ? 0 : 1);
+                dst = piece + wg * NC * D;
+                const float rf = my_ref();
+                if (qd == 0 && lane < NC) {
+                    piece[(size_t)NR * D + wg * NC + lane] = rf;
+                    piece[(size_t)NR * D + NR + wg * NC + lane] = L;
+                }
+            }
+            uint32_t rows = __ballot_sync(0xffffffffu, mine);
+            if (D == 64 && qd >= 2)
+                rows = 0;  // the upper lanes hold no channels
+            dst += run16(32 * qd + lane);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                const float f = __shfl_sync(0xffffffffu, scale, k);
+                if ((rows >> k) & 1u)
+#pragma unroll
+                    for (int x = 0; x < MH; ++x)
+                        dst[k * D + 128 * x] = o[x][k] * f;
+            }
+        };
+
+#pragma unroll 1
+        for (int i = -2; i < n; ++i) {  // -2 and -1: the keys of tiles 0 and 1, the values of 0
+            const AttDesc& d = s_desc[i & (kAttDescs - 1)];
+            if (i >= 0) {
+            if (i + 1 >= n)  // else it was waited for before the keys of tile i + 1
+                wait(&s_sdone[i & 1], i >> 1);
+            tc_fence_after();
+            if (__builtin_expect(d.first, 0)) {
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    if constexpr (C::REG_REF)
+                        ref[k] = -INFINITY;
+                    l[k] = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < MH; ++h)
+                        o[h][k] = 0.0f;
+                }
+                if constexpr (!C::REG_REF) {
+                    named_bar(3 + wg, 128);  // the previous row tile's are no longer read
+                    if (qd == 0)
+                        s_ref[wg][lane % NC] = -INFINITY;
+                    named_bar(3 + wg, 128);
+                }
+            }
+            // this warp's tokens: a quantized unit, or fp16 tokens
             const bool quant = qd < d.nuq;
-            const bool off = quant && !((d.umask >> qd) & 1u);
-            const int f = d.v0 + 32 * qd + lane - d.nq;          // fp16 token
-            const int j = f - d.res;                             // draft
+            const bool skip = quant && !((d.umask >> qd) & 1u);
+            const int j = d.f0 + 32 * qd + lane - d.res;  // draft, at or past 0
+            const bool masked = skip || (!quant && j >= 0);
+            uint32_t sees = 0u;                           // rows (bits) that attend this lane's token
+            if (__builtin_expect(masked && !skip && j < d.nd, 0)) {
+                const uint64_t* mw = a.mask + (size_t)d.b * a.N * W + (j >> 6);
+                int row = ((d.rr % pl.RT) * NR + wg * NC) % a.N;
+#pragma unroll 2
+                for (int k = 0; k < NC; ++k) {
+                    if (row < d.nd)
+                        sees |= (uint32_t)((ldg_checked(mw + (size_t)row * W) >> (j & 63)) & 1) << k;
+                    if (++row == a.N)
+                        row = 0;
+                }
+            }
+            __syncwarp();
             const uint32_t src = tm + C::TM_S + (i & 1) * NR + wg * NC + lanes;
             float y[CH];
-            auto load = [&](int k0) {
+            // -inf where the row does not attend the lane's token
+            auto apply_mask = [&](int k0) {
+                if (__builtin_expect(masked, 0)) {
+#pragma unroll
+                    for (int k = 0; k < CH; ++k)
+                        y[k] = (sees >> (k0 + k)) & 1u ? y[k] : -INFINITY;
+                }
+                __syncwarp();
+            };
+            auto exponents = [&](int k0) {
                 tc_ld(y, src + k0);
                 tc_wait_ld(y);
 #pragma unroll
                 for (int k = 0; k < CH; ++k)
-                    y[k] *= sl2;
-                if (off || (!quant && f >= d.res)) {
-                    const int W = (a.N + 63) >> 6;
-                    const bool draft = !off && j < d.nd;
-                    int row = (rt * NR + wg * NC + k0) % a.N;
+                    y[k] = __fmul_rn(y[k], sl2);
+                if constexpr (C::REG_REF) {
 #pragma unroll
-                    for (int k = 0; k < CH; ++k) {
-                        bool see = false;
-                        if (draft && row < d.nd)
-                            see = (ldg_checked(a.mask + ((size_t)d.b * a.N + row) * W + (j >> 6)) >> (j & 63)) & 1;
-                        if (!see)
-                            y[k] = -INFINITY;
-                        if (++row == a.N)
-                            row = 0;
+                    for (int k = 0; k < CH; ++k)
+                        y[k] -= ref[k0 + k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < CH; k += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&s_ref[wg][k0 + k]);
+                        y[k] -= f.x;
+                        y[k + 1] -= f.y;
+                        y[k + 2] -= f.z;
+                        y[k + 3] -= f.w;
                     }
                 }
-                __syncwarp();
+                apply_mask(k0);
             };
-            float mine = -INFINITY;
+            // the second time round, after the references moved, no weight passes the limit
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                float top = -INFINITY;
 #pragma unroll
-            for (int k0 = 0; k0 < NC; k0 += CH) {
-                load(k0);
+                for (int k0 = 0; k0 < NC; k0 += CH) {
+                    exponents(k0);
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const float x = redux_max(y[k]);
-                    if (lane == k0 + k)
-                        mine = x;
+                    for (int k = 0; k < CH; ++k)
+                        top = fmaxf(top, y[k]);
+                }
+                if (__builtin_expect(pass == 1 || !group_any(3 + wg, top > kAttLimit), 1))
+                    break;
+                float mine = -INFINITY;  // the warp's largest logit of row `lane`
+#pragma unroll
+                for (int k0 = 0; k0 < NC; k0 += CH) {
+                    tc_ld(y, src + k0);
+                    tc_wait_ld(y);
+#pragma unroll
+                    for (int k = 0; k < CH; ++k)
+                        y[k] = __fmul_rn(y[k], sl2);
+                    apply_mask(k0);
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) {
+                        const float x = redux_max(y[k]);
+                        mine = lane == k0 + k ? x : mine;
+                    }
+                }
+                const float old = my_ref();
+                if (lane < NC)
+                    s_red[wg][lane][qd] = mine;
+                named_bar(3 + wg, 128);
+                const float4 r = *reinterpret_cast<const float4*>(s_red[wg][lane < NC ? lane : 0]);
+                const float m = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
+                // a maximum beyond 2^20 is its own reference: 13 would be lost in it
+                const float next = fmaxf(old, fabsf(m) < 1048576.0f ? m - kAttShift : m);
+                const float alpha = next == old ? 1.0f : ex2(old - next);
+                if constexpr (!C::REG_REF) {
+                    if (qd == 0)
+                        s_ref[wg][lane % NC] = next;  // every warp has read the old one
+                    named_bar(3 + wg, 128);
+                }
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    if constexpr (C::REG_REF)
+                        ref[k] = __shfl_sync(0xffffffffu, next, k);
+                    const float f = __shfl_sync(0xffffffffu, alpha, k);
+                    l[k] *= f;
+#pragma unroll
+                    for (int h = 0; h < MH; ++h)
+                        o[h][k] *= f;
                 }
             }
-            if (lane < NC)
-                s_red[0][wg][lane][qd] = mine;
-            named_bar(2 + wg, 128);
-            const float4 r = *reinterpret_cast<const float4*>(s_red[0][wg][lane < NC ? lane : 0]);
-            const float mn = fmaxf(fmaxf(m, fmaxf(r.x, r.y)), fmaxf(r.z, r.w));
-            const float ref = mn == -INFINITY ? 0.0f : mn;
-            alpha = m == mn ? 1.0f : ex2(m - ref);
-            m = mn;
-            const float sub = ref - kAttShift;
-            const bool grew = __any_sync(0xffffffffu, alpha != 1.0f && lane < NC);
             uint8_t* prow = sm + C::O_P + (32 * qd + lane) * 128;
-            const int sw = lane & 7;  // token % 8
+            const int sw = lane & 7;  // token position % 8
 #pragma unroll
             for (int k0 = 0; k0 < NC; k0 += CH) {
                 if (NC > CH)
-                    load(k0);
+                    exponents(k0);
                 uint32_t hi[CH / 2], lo[CH / 2];
 #pragma unroll
                 for (int k = 0; k < CH; k += 2) {
-                    const float p0 = ex2(y[k] - __shfl_sync(0xffffffffu, sub, k0 + k));
-                    const float p1 = ex2(y[k + 1] - __shfl_sync(0xffffffffu, sub, k0 + k + 1));
-                    if (grew) {
-                        l[k0 + k] *= __shfl_sync(0xffffffffu, alpha, k0 + k);
-                        l[k0 + k + 1] *= __shfl_sync(0xffffffffu, alpha, k0 + k + 1);
-                    }
+                    const float p0 = ex2(y[k]), p1 = ex2(y[k + 1]);
                     l[k0 + k] += p0;
                     l[k0 + k + 1] += p1;
                     split_hi_lo(p0, p1, hi[k / 2], lo[k / 2]);
                 }
+                const int r0 = wg * NC + k0;
+                if constexpr (NC < 8) {  // half a 16-byte chunk of each term
+                    const int at = (r0 & 4) << 1;
+                    *reinterpret_cast<uint2*>(prow + (((r0 >> 3) ^ sw) << 4) + at) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(prow + (((NR / 8 + (r0 >> 3)) ^ sw) << 4) + at) = make_uint2(lo[0], lo[1]);
+                } else {
 #pragma unroll
-                for (int k = 0; k < CH; k += 8) {
-                    const int r0 = wg * NC + k0 + k;  // first of eight rows: one 16-byte chunk of each term
-                    uint8_t* h0 = prow + (r0 >> 6) * kAttAtom;
-                    const uint4 vh = make_uint4(hi[k / 2], hi[k / 2 + 1], hi[k / 2 + 2], hi[k / 2 + 3]);
-                    const uint4 vl = make_uint4(lo[k / 2], lo[k / 2 + 1], lo[k / 2 + 2], lo[k / 2 + 3]);
-                    *reinterpret_cast<uint4*>(h0 + ((((r0 >> 3) & 7) ^ sw) << 4)) = vh;
-                    if constexpr (C::STACK)
-                        *reinterpret_cast<uint4*>(h0 + (((4 + (r0 >> 3)) ^ sw) << 4)) = vl;
-                    else
-                        *reinterpret_cast<uint4*>(h0 + (C::PATOMS / 2) * kAttAtom + ((((r0 >> 3) & 7) ^ sw) << 4)) = vl;
+                    for (int k = 0; k < CH; k += 8) {  // eight rows: a 16-byte chunk of each term
+                        const int ck = (r0 + k) >> 3;
+                        uint8_t* row = prow + (ck >> 3) * C::PATOM;
+                        const uint4 vh = make_uint4(hi[k / 2], hi[k / 2 + 1], hi[k / 2 + 2], hi[k / 2 + 3]);
+                        const uint4 vl = make_uint4(lo[k / 2], lo[k / 2 + 1], lo[k / 2 + 2], lo[k / 2 + 3]);
+                        *reinterpret_cast<uint4*>(row + (((ck & 7) ^ sw) << 4)) = vh;
+                        if constexpr (C::STACK)
+                            *reinterpret_cast<uint4*>(row + (((NR / 8 + ck) ^ sw) << 4)) = vl;
+                        else
+                            *reinterpret_cast<uint4*>(row + C::PTERM + (((ck & 7) ^ sw) << 4)) = vl;
+                    }
                 }
             }
-        };
-
-        // O of tile i joins the running output; the row tile's last one writes it
-        auto output = [&](int i) {
-            const AttDesc& d = s_desc[i & (kAttDescs - 1)];
-            const bool grew = __any_sync(0xffffffffu, alpha != 1.0f && lane < NC);
+            publish();  // O(i) is issued
+            }
+            if (i + 2 < n) {
+                if (i >= -1)
+                    wait(&s_sdone[(i + 1) & 1], (i + 1) >> 1);
+                keys(i + 2);
+                publish();  // S(i + 2) is issued
+            }
+            if (i >= 0) {
+            wait(&s_odone, i);
+            tc_fence_after();
+            constexpr int OC = NC < 8 ? NC : 8;
 #pragma unroll
             for (int h = 0; h < MH; ++h)
 #pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += CH) {
-                    float t[CH];
+                for (int k0 = 0; k0 < NC; k0 += OC) {
+                    float y[OC];
                     const uint32_t src = tm + C::TM_O + h * C::PN + wg * NC + k0 + lanes;
-                    tc_ld(t, src);
+                    tc_ld(y, src);
                     if constexpr (C::STACK) {
-                        float t2[CH];
-                        tc_ld(t2, src + 32);
-                        tc_wait_ld(t);
-                        tc_wait_ld(t2);
+                        float z[OC];
+                        tc_ld(z, src + NR);
+                        tc_wait_ld(y);
+                        tc_wait_ld(z);
 #pragma unroll
-                        for (int k = 0; k < CH; ++k)
-                            t[k] += t2[k];
+                        for (int k = 0; k < OC; ++k)
+                            y[k] += z[k];
                     } else {
-                        tc_wait_ld(t);
+                        tc_wait_ld(y);
                     }
-                    if (d.first) {
 #pragma unroll
-                        for (int k = 0; k < CH; ++k)
-                            o[h][k0 + k] = t[k];
-                    } else if (grew) {
-#pragma unroll
-                        for (int k = 0; k < CH; ++k)
-                            o[h][k0 + k] = fmaf(o[h][k0 + k], __shfl_sync(0xffffffffu, alpha, k0 + k), t[k]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < CH; ++k)
-                            o[h][k0 + k] += t[k];
-                    }
+                    for (int k = 0; k < OC; ++k)
+                        o[h][k0 + k] += y[k];
                 }
-            if (!d.last)
-                return;
-            float sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                float x = l[k];
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1)
-                    x += __shfl_xor_sync(0xffffffffu, x, s);
-                if (lane == k)
-                    sum = x;
+            if (__builtin_expect(d.last, 0)) {
+                finish(i);
+                named_bar(2, C::WORKERS);  // P's buffer, where the sums went, may be written
             }
-            if (lane < NC)
-                s_red[1][wg][lane][qd] = sum;
-            named_bar(2 + wg, 128);
-            const float4 r = *reinterpret_cast<const float4*>(s_red[1][wg][lane < NC ? lane : 0]);
-            const float L = (r.x + r.y) + (r.z + r.w);
-            const int h = d.rr / pl.RT, r0 = (d.rr - h * pl.RT) * NR + wg * NC;
-            const int ch = 32 * qd + lane;
-            const bool owns = D >= 128 || qd < 2;  // D = 64: the upper lanes hold no channels
-            if (d.tail && !d.mid) {
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                float* dst = a.out + (((size_t)d.b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + r0) * D + ch;
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const float f = __shfl_sync(0xffffffffu, inv, k);
-                    if (owns && r0 + k < pl.M && (!a.k || (r0 + k) % a.N < d.nd))
-#pragma unroll
-                        for (int x = 0; x < MH; ++x)
-                            st_checked(dst + (size_t)k * D + 128 * x, o[x][k] * f);
-                }
-            } else {
-                // a piece: slot 0 for a row tile that an earlier CTA starts, else 1
-                float* part = att_part(ws, D, NR, (int)cta, d.mid ? 0 : 1);
-                if (owns) {
-#pragma unroll
-                    for (int k = 0; k < NC; ++k)
-#pragma unroll
-                        for (int x = 0; x < MH; ++x)
-                            part[(size_t)(wg * NC + k) * D + ch + 128 * x] = o[x][k];
-                }
-                if (qd == 0 && lane < NC) {
-                    part[(size_t)NR * D + wg * NC + lane] = m;
-                    part[(size_t)NR * D + NR + wg * NC + lane] = L;
-                }
             }
-        };
-
-        if (tid == 0)
-            for (int i = 0; i < 4; ++i)
-                describe();
-        barrier();
-        keys(0);
-        publish();
-        issue_s(0);
-        if (n > 1) {
-            wait(&s_sbar[0], 0);
-            keys(1);
-            publish();
-            issue_s(1);
-        }
-        values(0);
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            if (tid == 0)
-                describe();  // tile i + 4
-            wait(&s_sbar[i & 1], i >> 1);
-            tc_fence_after();
-            softmax(i);
-            publish();
-            issue_o();
-            if (i + 2 < n) {
-                wait(&s_sbar[(i + 1) & 1], (i + 1) >> 1);
-                keys(i + 2);
-                publish();
-                issue_s(i + 2);
-            }
-            wait(&s_obar, i);
-            tc_fence_after();
-            output(i);
-            if (i + 1 < n)
+            if (i >= -1 && i + 1 < n)
                 values(i + 1);
-        }
-        if (*(volatile int*)&s_abort) {  // products in flight end before their TMEM is freed
-            mbar_wait_bounded(&s_sbar[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_never);
-            mbar_wait_bounded(&s_obar, (n - 1) & 1, &s_never);
         }
         tc_fence_before();
     }
     asm volatile("griddepcontrol.launch_dependents;");
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tc_dealloc(tm, C::TM_COLS);
     }
@@ -984,17 +1098,18 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
     if (cut[0] == 0)
         return;
     const int b = cut[1], rr = cut[2], last = cut[3];
-    const long long total = (long long)cut[4] | (long long)cut[5] << 31, N = gridDim.x;
     const int h = rr / pl.RT, rt = rr - h * pl.RT;
     const int nd = a.k ? (a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), a.N) : a.N) : 1;
+#pragma unroll 1
     for (int e = threadIdx.x; e < kAttCombineRows * D; e += kAttCombineThreads) {
         const int r = blockIdx.y * kAttCombineRows + e / D, d = e % D, row = rt * NR + r;
         if (row >= pl.M || row % a.N >= nd)
             continue;
         float M = -INFINITY, L = 0.0f, o = 0.0f;
+#pragma unroll 1
         for (int k = i; k <= last; ++k) {
-            if (total * k / N == total * (k + 1) / N)
-                continue;
+            if (cut[(k - i) * kAttCutInts + 4] == 0)
+                continue;  // an empty range
             const float* p = att_part(ws, D, NR, k, k == i);
             const float m = p[(size_t)NR * D + r], l = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
             if (m == -INFINITY)
@@ -1010,25 +1125,32 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
 
 // ----------------------------------------------------------------- launch ---
 
-template <int D, int NR>
+template <int D, int NR, int B>
 cudaError_t attend_launch_rows(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
 {
     using C = AttCfg<D, NR>;
-    auto kern = attend_kernel<D, NR>;
+    auto kern = attend_kernel<D, NR, B>;
     AttPlan pl;
     pl.lgG = c.G == 32 ? 5 : c.G == 64 ? 6 : 7;
     pl.M = a.Hq / c.H * a.N;
     pl.RT = (pl.M + NR - 1) / NR;
     pl.kub = 4 * D * c.bits_k;
     pl.vub = 4 * D * c.bits_v;
-    pl.stage = cmax(4 * pl.kub + 32 * D, 4 * pl.vub + 1024 * (D / c.G));
-    pl.ns = cmin(C::RING / pl.stage, kAttMaxStages);
-    const int smem = 1024 + C::O_RING + pl.ns * pl.stage;
+    for (pl.su = 4;; pl.su = 2) {  // a tile per stage where one fits, else half a tile
+        pl.kst = pl.su * (pl.kub + 8 * D);
+        pl.vst = pl.su * (pl.vub + 256 * (D / c.G));
+        pl.ns = cmin(C::RING / (pl.kst + pl.vst), kAttMaxStages);
+        if (pl.ns > 0 || pl.su == 2)
+            break;
+    }
+    if (pl.ns < 1)
+        return cudaErrorInvalidConfiguration;
+    const int smem = 1024 + C::O_RING + pl.ns * (pl.kst + pl.vst);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    const int N = cmin(sm_count(), kAttMaxCTAs);
-    kern<<<N, kAttThreads, smem, s>>>(c, a, pl, ws);
+    const int N = cmin(C::CTAS * sm_count(), kAttMaxCTAs);
+    kern<<<N, C::THREADS, smem, s>>>(c, a, pl, ws);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -1045,28 +1167,41 @@ cudaError_t attend_launch_rows(const kivi_cache& c, const AttendArgs& a, float* 
     return cudaLaunchKernelEx(&cfg, attend_combine_kernel, c, a, pl, NR, ws);
 }
 
-template <int D>
-cudaError_t launch_attend_d(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
+template <int D, int B>
+cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
 {
     KIVI_SET_CHECK_RANGES(c, s, {{a.q, (size_t)c.B * a.Hq * a.N * D * 2}, {a.out, (size_t)c.B * a.Hq * a.N * D * 4},
                                  {a.k, (size_t)c.B * c.H * a.N * D * 2}, {a.v, (size_t)c.B * c.H * a.N * D * 2},
                                  {a.mask, (size_t)c.B * a.N * ((a.N + 63) / 64) * 8}, {a.n_draft, (size_t)c.B * 4},
                                  {a.blocks, (size_t)c.B * c.H * a.n_keep * 4}});
     switch (attend_rows(D, a.Hq / c.H * a.N)) {
-    case 32: return attend_launch_rows<D, 32>(c, a, ws, s);
+    case 16: return attend_launch_rows<D, 16, B>(c, a, ws, s);
+    case 32: return attend_launch_rows<D, 32, B>(c, a, ws, s);
     case 64:
         if constexpr (D != 256)
-            return attend_launch_rows<D, 64>(c, a, ws, s);
+            return attend_launch_rows<D, 64, B>(c, a, ws, s);
         break;
     default:
         if constexpr (D != 256)
-            return attend_launch_rows<D, 128>(c, a, ws, s);
+            return attend_launch_rows<D, 128, B>(c, a, ws, s);
         break;
     }
     return cudaErrorInvalidValue;
 }
 
-#define KIVI_ATTEND_INSTANTIATE(DIM) \
-    template cudaError_t launch_attend_d<DIM>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t);
+// Instantiates the kernels of one head dimension and code width (0: mixed), a
+// translation unit each, so that they compile in parallel.
+#ifdef KIVI_CHECKS
+#define KIVI_ATTEND_INSTANTIATE(DIM, B)                                                                       \
+    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t); \
+    template <>                                                                                               \
+    int32_t check_word_attend_b<DIM, B>()                                                                     \
+    {                                                                                                         \
+        return take_check_word();                                                                             \
+    }
+#else
+#define KIVI_ATTEND_INSTANTIATE(DIM, B) \
+    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t);
+#endif
 
 }  // namespace kivi

@@ -1,0 +1,8 @@
+// attend_d256_mixed.cu -- sparse and tree attention, head dimension 256, key and value widths that differ.
+#include "attend.cuh"
+
+namespace kivi {
+
+KIVI_ATTEND_INSTANTIATE(256, 0)
+
+}  // namespace kivi

@@ -1,0 +1,8 @@
+// attend_d64_b8.cu -- sparse and tree attention, head dimension 64, 8-bit codes.
+#include "attend.cuh"
+
+namespace kivi {
+
+KIVI_ATTEND_INSTANTIATE(64, 8)
+
+}  // namespace kivi

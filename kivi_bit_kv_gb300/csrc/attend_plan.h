@@ -1,0 +1,90 @@
+// attend_plan.h -- shapes of the sparse and tree attention kernel (attend.cuh):
+// its roles, shared memory, TMEM and workspace.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define KIVI_HD __host__ __device__
+#else
+#define KIVI_HD
+#endif
+
+namespace kivi {
+
+constexpr int kAttSmem = 227 * 1024;          // shared memory of one CTA alone on its SM
+constexpr int kAttTile = 128;                 // tokens per tile
+constexpr int kAttMaxCTAs = 320;              // workspace bound on the grid
+constexpr int kAttMaxStages = 8;              // of each ring
+constexpr int kAttDescs = 16;                 // tile descriptors kept in shared memory
+constexpr int kAttCutInts = 8;
+constexpr int kAttHeaderFloats = 4;
+constexpr float kAttShift = 13.0f;            // a row's largest weight is 2^13 when its reference is set ...
+constexpr float kAttLimit = 15.9f;            // ... and stays below 2^15.9, inside fp16
+
+// Rows per row tile for M query rows of a KV head.
+inline int attend_rows(int D, int M)
+{
+    return M <= 16 ? 16 : M <= 32 || D == 256 ? 32 : M <= 64 ? 64 : 128;
+}
+
+// Workspace: header (status word), a cut descriptor per CTA, two partial
+// (o [NR][D], m [NR], l [NR]) slots per CTA: slot 0 for a row tile that an
+// earlier CTA started, slot 1 for one that starts here and ends later.
+KIVI_HD inline float* att_part(float* ws, int D, int NR, int cta, int slot)
+{
+    return ws + kAttHeaderFloats + kAttMaxCTAs * kAttCutInts + ((size_t)cta * 2 + slot) * NR * (D + 2);
+}
+
+// A CTA has 8 or 16 worker warps, two copy warps (keys, values) and the MMA
+// warp.  A tile passes through a chain of steps with a barrier or a wait
+// between any two, so where shared memory allows (D <= 128, up to 32 rows) two
+// CTAs of 8 worker warps share an SM: one computes while the other waits,
+// starts a row or ends one.
+template <int D, int NR>
+struct AttCfg {
+    static constexpr int CTAS = D <= 128 && NR <= 32 ? 2 : 1;  // CTAs per SM
+    static constexpr int WORKERS = CTAS == 2 ? 256 : 512;
+    static constexpr int THREADS = WORKERS + 96;
+    static constexpr int GROUPS = WORKERS / 128;       // row groups
+    static constexpr int MH = D == 256 ? 2 : 1;        // 128-channel halves of the output
+    static constexpr int NC = NR / GROUPS;             // rows of a worker warp
+    static constexpr int CH = NC < 16 ? NC : 16;       // rows of one TMEM read
+    static constexpr bool REG_REF = NC <= 16;
+    static constexpr bool STACK = NR <= 32;            // both terms of P side by side in one product
+    static constexpr int PN = NR <= 64 ? 64 : NR;      // columns of the second product
+    static constexpr int PASSES = STACK ? 1 : 2;
+    static constexpr int KBYTES = 256 * D;             // 64-token columns of D x 128 bytes
+    static constexpr int VATOM = kAttTile * 128;       // 64-channel columns of 128 x 128 bytes
+    static constexpr int VBYTES = VATOM * (D == 64 ? 2 : D / 64);  // the M axis has 128 rows at least
+    static constexpr int PATOM = kAttTile * 128;       // 64 columns of P
+    static constexpr int PTERM = PATOM * PN / 64;      // one term of P
+    static constexpr int PBYTES = PTERM * PASSES;
+    static constexpr int QBYTES = D / 64 * NR * 128;
+    static constexpr int O_K = 0;
+    static constexpr int O_V = O_K + KBYTES;
+    static constexpr int O_P = O_V + VBYTES;
+    static constexpr int O_Q = O_P + PBYTES;
+    static constexpr int O_RING = O_Q + QBYTES;
+    static constexpr int TM_S = 0;                     // TMEM columns: S of even and odd tiles, O
+    static constexpr int TM_O = 2 * NR;
+    static constexpr int TM_USED = TM_O + MH * PN;
+    static constexpr int TM_COLS = TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
+    // 1024: base alignment; an SM has 228 KB, of which every CTA takes one more
+    static constexpr int STATIC = (CTAS == 2 ? 3 : 6) * 1024;  // bound on the kernel's static shared arrays
+    static constexpr int RING = (CTAS == 2 ? 113 * 1024 : kAttSmem) - STATIC - 1024 - O_RING;
+    static_assert(O_Q % 1024 == 0 && QBYTES % 1024 == 0 && O_P % 1024 == 0, "operand alignment");
+    static_assert(D != 256 || NR <= 32, "shared memory");
+};
+
+// Sizes the kernel needs besides the descriptor's.
+struct AttPlan {
+    int lgG, M, RT;       // log2 G, query rows of a KV head, row tiles
+    int su;               // 32-token units of a ring stage: a tile's four, or two
+    int ns;               // stages of each ring
+    int kst, vst;         // bytes of a stage: keys, values
+    int kub, vub;         // code bytes of 32 tokens: keys, values
+};
+
+}  // namespace kivi

@@ -44,9 +44,10 @@ struct AttendArgs {
     int32_t Hq, N, n_keep;
 };
 cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cudaStream_t s);
-// The same for one head dimension; instantiated in attend_d<D>.cu.
-template <int D>
-cudaError_t launch_attend_d(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s);
+// The same for one head dimension and code width (0: keys and values differ);
+// instantiated in attend_d<D>_*.cu.
+template <int D, int B>
+cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s);
 size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N);
 cudaError_t launch_decode_qk(const kivi_cache& c, const uint16_t* q, int Hq, float sm_scale,
                              float* logits, int ld_logits, cudaStream_t s);
@@ -102,9 +103,9 @@ int32_t check_word_decode_d64();
 int32_t check_word_decode_d128();
 int32_t check_word_decode_d256();
 int32_t check_word_select();
-int32_t check_word_attend_d64();
-int32_t check_word_attend_d128();
-int32_t check_word_attend_d256();
+template <int D, int B>
+int32_t check_word_attend_b();
+int32_t check_word_attend();
 #endif
 
 // Sets the message kivi_last_error() returns on this host thread; returns status.
