@@ -7,9 +7,11 @@ namespace kivi {
 
 size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N)
 {
-    const int NR = attend_rows(c.D, Hq / c.H * N);
-    return ((size_t)kAttHeaderFloats + (size_t)kAttMaxCTAs * kAttCutInts +
-            (size_t)kAttMaxCTAs * 2 * NR * (c.D + 2)) * sizeof(float);
+    const int M = Hq / c.H * N;
+    const bool warp = attend_by_warp(c.D, M);
+    const size_t pieces = warp ? kAttMaxRanges : kAttMaxCTAs;
+    const size_t floats = warp ? warp_part_floats(c.D, M) : (size_t)attend_rows(c.D, M) * (c.D + 2);
+    return (kAttHeaderFloats + pieces * (kAttCutInts + 2 * floats)) * sizeof(float);
 }
 
 template <int D>

@@ -241,8 +241,9 @@ __device__ __forceinline__ void att_next(AttWalk& w, const kivi_cache& c, const 
     }
 }
 
-// One warp: the CTA's range of tiles [range[0], range[1]), the total range[2],
-// and the position of the range's first tile.
+// One warp: the CTA's range of tiles [range[0], range[1]) of range[2], one of
+// range[3] = min(CTAs, total) ranges (none for a CTA beyond them), and the
+// position of its first tile.
 static __device__ __noinline__ void att_locate(const kivi_cache* c, const AttendArgs* a, const AttPlan* pl,
                                                long long* range, AttWalk* first)
 {
@@ -257,12 +258,16 @@ static __device__ __noinline__ void att_locate(const kivi_cache* c, const Attend
             n += __shfl_xor_sync(0xffffffffu, n, o);
         total += n;
     }
-    const long long p = total * blockIdx.x / gridDim.x;
+    const long long index = blockIdx.x, count = min((long long)gridDim.x, total);
+    const long long p = index < count ? total * index / count : total;
     if (lane == 0) {
         range[0] = p;
-        range[1] = total * (blockIdx.x + 1) / gridDim.x;
+        range[1] = index < count ? total * (index + 1) / count : total;
         range[2] = total;
+        range[3] = count;
     }
+    if (p == total)
+        return;
     long long before = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < c->B; b0 += 32) {
@@ -546,12 +551,12 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_never;
     __shared__ AttWalk s_walk;
-    __shared__ long long s_range[3];
+    __shared__ long long s_range[4];
     uint8_t* sm = att_smem + ((1024u - (smem_addr(att_smem) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int RB = c.H * pl.RT;
     int* status = reinterpret_cast<int*>(ws);
-    const long long ctas = gridDim.x, cta = blockIdx.x;
+    const long long cta = blockIdx.x;
 
     if (warp == kCopyWarp) {
         att_locate(&c, &a, &pl, s_range, &s_walk);
@@ -592,10 +597,8 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
         const bool starts_mid = w.j > 0;
         const int b0 = w.b, rr0 = w.rr;
         int* cut = reinterpret_cast<int*>(ws + kAttHeaderFloats) + (size_t)cta * kAttCutInts;
-        if (warp == kCopyWarp && lane == 0) {
+        if (warp == kCopyWarp && lane == 0)
             cut[0] = 0;
-            cut[4] = n;
-        }
         // a unit: 32 tokens' codes, then its scales, then its zeros, at these
         // byte strides per 32 tokens (keys: statistics per group)
         const uint32_t code = which == 0 ? pl.kub : pl.vub;
@@ -647,15 +650,12 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 d.last = d.tail || i == n - 1;
                 d.umask = mask;
                 if (__builtin_expect(i == n - 1 && !d.tail && !d.mid, 0)) {
-                    // the row tile starts in this range and ends in a later one, at tile `end`
+                    // the row tile starts in this range and its last tile, end - 1, is in range
+                    // `last`: the first with total (last + 1) / count >= end
                     const long long end = s_range[1] + (w.s.nt - 1 - w.j);
-                    int k = (int)cta + 1;
-#pragma unroll 1
-                    while (s_range[2] * (k + 1) / ctas < end)
-                        ++k;
                     cut[1] = w.b;
                     cut[2] = w.rr;
-                    cut[3] = k;
+                    cut[3] = (int)((end * s_range[3] + s_range[2] - 1) / s_range[2] - 1);
                     cut[0] = 1;
                 }
                 }
@@ -1086,7 +1086,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
 
 // Merges the pieces of the row tiles that CTA ranges cut: block (i, y) takes
 // eight rows of the row tile that starts in range i and ends in a later one,
-// piece by piece in order (empty ranges hold none).
+// piece by piece in order.
 constexpr int kAttCombineThreads = 256;
 constexpr int kAttCombineRows = 8;
 static __global__ void __launch_bounds__(kAttCombineThreads)
@@ -1108,8 +1108,6 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
         float M = -INFINITY, L = 0.0f, o = 0.0f;
 #pragma unroll 1
         for (int k = i; k <= last; ++k) {
-            if (cut[(k - i) * kAttCutInts + 4] == 0)
-                continue;  // an empty range
             const float* p = att_part(ws, D, NR, k, k == i);
             const float m = p[(size_t)NR * D + r], l = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
             if (m == -INFINITY)
@@ -1166,42 +1164,5 @@ cudaError_t attend_launch_rows(const kivi_cache& c, const AttendArgs& a, float* 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attend_combine_kernel, c, a, pl, NR, ws);
 }
-
-template <int D, int B>
-cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
-{
-    KIVI_SET_CHECK_RANGES(c, s, {{a.q, (size_t)c.B * a.Hq * a.N * D * 2}, {a.out, (size_t)c.B * a.Hq * a.N * D * 4},
-                                 {a.k, (size_t)c.B * c.H * a.N * D * 2}, {a.v, (size_t)c.B * c.H * a.N * D * 2},
-                                 {a.mask, (size_t)c.B * a.N * ((a.N + 63) / 64) * 8}, {a.n_draft, (size_t)c.B * 4},
-                                 {a.blocks, (size_t)c.B * c.H * a.n_keep * 4}});
-    switch (attend_rows(D, a.Hq / c.H * a.N)) {
-    case 16: return attend_launch_rows<D, 16, B>(c, a, ws, s);
-    case 32: return attend_launch_rows<D, 32, B>(c, a, ws, s);
-    case 64:
-        if constexpr (D != 256)
-            return attend_launch_rows<D, 64, B>(c, a, ws, s);
-        break;
-    default:
-        if constexpr (D != 256)
-            return attend_launch_rows<D, 128, B>(c, a, ws, s);
-        break;
-    }
-    return cudaErrorInvalidValue;
-}
-
-// Instantiates the kernels of one head dimension and code width (0: mixed), a
-// translation unit each, so that they compile in parallel.
-#ifdef KIVI_CHECKS
-#define KIVI_ATTEND_INSTANTIATE(DIM, B)                                                                       \
-    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t); \
-    template <>                                                                                               \
-    int32_t check_word_attend_b<DIM, B>()                                                                     \
-    {                                                                                                         \
-        return take_check_word();                                                                             \
-    }
-#else
-#define KIVI_ATTEND_INSTANTIATE(DIM, B) \
-    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t);
-#endif
 
 }  // namespace kivi

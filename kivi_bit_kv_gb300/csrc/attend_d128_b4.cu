@@ -1,5 +1,5 @@
 // attend_d128_b4.cu -- sparse and tree attention, head dimension 128, 4-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

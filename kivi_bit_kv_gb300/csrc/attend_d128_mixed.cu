@@ -1,5 +1,5 @@
 // attend_d128_mixed.cu -- sparse and tree attention, head dimension 128, key and value widths that differ.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

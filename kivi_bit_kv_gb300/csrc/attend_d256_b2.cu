@@ -1,5 +1,5 @@
 // attend_d256_b2.cu -- sparse and tree attention, head dimension 256, 2-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

@@ -1,5 +1,5 @@
 // attend_d256_b8.cu -- sparse and tree attention, head dimension 256, 8-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

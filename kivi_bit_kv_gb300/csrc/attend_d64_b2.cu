@@ -1,5 +1,5 @@
 // attend_d64_b2.cu -- sparse and tree attention, head dimension 64, 2-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

@@ -1,5 +1,5 @@
 // attend_d64_b4.cu -- sparse and tree attention, head dimension 64, 4-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

@@ -1,5 +1,5 @@
 // attend_d64_b8.cu -- sparse and tree attention, head dimension 64, 8-bit codes.
-#include "attend.cuh"
+#include "attend_launch.cuh"
 
 namespace kivi {
 

@@ -1,0 +1,54 @@
+// attend_launch.cuh -- which kernel serves a call of kivi_sparse_attention or
+// kivi_tree_attention.
+#pragma once
+
+#include "attend_warp.cuh"
+
+namespace kivi {
+
+// Up to 16 query rows of a KV head (8 at D = 256) go to the warp kernel, more
+// to the tcgen05 kernel, whose products cost the same up to 32 rows.
+template <int D, int B>
+cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
+{
+    KIVI_SET_CHECK_RANGES(c, s, {{a.q, (size_t)c.B * a.Hq * a.N * D * 2}, {a.out, (size_t)c.B * a.Hq * a.N * D * 4},
+                                 {a.k, (size_t)c.B * c.H * a.N * D * 2}, {a.v, (size_t)c.B * c.H * a.N * D * 2},
+                                 {a.mask, (size_t)c.B * a.N * ((a.N + 63) / 64) * 8}, {a.n_draft, (size_t)c.B * 4},
+                                 {a.blocks, (size_t)c.B * c.H * a.n_keep * 4}});
+    const int M = a.Hq / c.H * a.N;
+    if (attend_by_warp(D, M)) {
+        if constexpr (D != 256)
+            if (M > 8)
+                return attend_warp_launch<D, 2, B>(c, a, ws, s);
+        return attend_warp_launch<D, 1, B>(c, a, ws, s);
+    }
+    switch (attend_rows(D, M)) {
+    case 32: return attend_launch_rows<D, 32, B>(c, a, ws, s);
+    case 64:
+        if constexpr (D != 256)
+            return attend_launch_rows<D, 64, B>(c, a, ws, s);
+        break;
+    default:
+        if constexpr (D != 256)
+            return attend_launch_rows<D, 128, B>(c, a, ws, s);
+        break;
+    }
+    return cudaErrorInvalidValue;
+}
+
+// Instantiates the kernels of one head dimension and code width (0: mixed), a
+// translation unit each, so that they compile in parallel.
+#ifdef KIVI_CHECKS
+#define KIVI_ATTEND_INSTANTIATE(DIM, B)                                                                       \
+    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t); \
+    template <>                                                                                               \
+    int32_t check_word_attend_b<DIM, B>()                                                                     \
+    {                                                                                                         \
+        return take_check_word();                                                                             \
+    }
+#else
+#define KIVI_ATTEND_INSTANTIATE(DIM, B) \
+    template cudaError_t launch_attend_b<DIM, B>(const kivi_cache&, const AttendArgs&, float*, cudaStream_t);
+#endif
+
+}  // namespace kivi

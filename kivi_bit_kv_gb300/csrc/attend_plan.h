@@ -23,11 +23,12 @@ constexpr int kAttHeaderFloats = 4;
 constexpr float kAttShift = 13.0f;            // a row's largest weight is 2^13 when its reference is set ...
 constexpr float kAttLimit = 15.9f;            // ... and stays below 2^15.9, inside fp16
 
-// Rows per row tile for M query rows of a KV head.
-inline int attend_rows(int D, int M)
-{
-    return M <= 16 ? 16 : M <= 32 || D == 256 ? 32 : M <= 64 ? 64 : 128;
-}
+// Whether M query rows of a KV head go to the warp kernel (attend_warp.cuh),
+// whose registers hold O of 16 rows (8 at D = 256).
+inline bool attend_by_warp(int D, int M) { return M <= (D == 256 ? 8 : 16); }
+
+// Rows per row tile of the tcgen05 kernel (attend.cuh) for M query rows.
+inline int attend_rows(int D, int M) { return M <= 32 || D == 256 ? 32 : M <= 64 ? 64 : 128; }
 
 // Workspace: header (status word), a cut descriptor per CTA, two partial
 // (o [NR][D], m [NR], l [NR]) slots per CTA: slot 0 for a row tile that an
@@ -35,6 +36,14 @@ inline int attend_rows(int D, int M)
 KIVI_HD inline float* att_part(float* ws, int D, int NR, int cta, int slot)
 {
     return ws + kAttHeaderFloats + kAttMaxCTAs * kAttCutInts + ((size_t)cta * 2 + slot) * NR * (D + 2);
+}
+
+// The same for the warp kernel: descriptors and slots of every warp, M rows.
+constexpr int kAttMaxRanges = kAttMaxCTAs / 2 * 16;
+KIVI_HD inline size_t warp_part_floats(int D, int M) { return (size_t)(M * (D + 2) + 3) / 4 * 4; }
+KIVI_HD inline float* warp_part(float* ws, int D, int M, long long range, int slot)
+{
+    return ws + kAttHeaderFloats + kAttMaxRanges * kAttCutInts + ((size_t)range * 2 + slot) * warp_part_floats(D, M);
 }
 
 // A CTA has 8 or 16 worker warps, two copy warps (keys, values) and the MMA
