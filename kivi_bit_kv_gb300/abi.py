@@ -301,32 +301,56 @@ def kivi_decode_attention(cache, q: torch.Tensor, out: torch.Tensor, ws: torch.T
            "kivi_decode_attention")
 
 
-def _shape(t: torch.Tensor, name: str, *shapes):
+# The calls of a decode step are a few microseconds of GPU work, so the checks
+# below cost little when they pass: shapes compare as tuples, a tensor's other
+# properties in one expression (_dev says which one is wrong), and the current
+# stream is asked for as a raw handle.
+
+def _bad_shape(t, name: str, *shapes):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) not in shapes:
-        raise ValueError(f"{name} shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
+    raise ValueError(f"{name} shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
 
 
-def _ws(ws: torch.Tensor, device):
-    return _dev(ws, ws.dtype, "ws", device), ws.numel() * ws.element_size()
+def _ptr(t: torch.Tensor, dtype, name: str, device) -> int:
+    if t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, name, device)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream, device)
+
+
+def _call(fn, where: str, device, *args):
+    """fn(*args) with the cache's device current, as the library requires."""
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != KIVI_OK:
+        _check(st, where)
 
 
 def kivi_block_select(cache, q: torch.Tensor, blocks: torch.Tensor, scores: torch.Tensor, stream=None):
     """blocks int32 [B, H, n_keep] <- the quantized key groups of largest score,
     ascending and padded with -1; scores fp32 [B, H, Tmax/G] <- the scores, an
     upper bound of q . k over each group; q fp16 [B, Hq, D] (or [B, Hq, 1, D])."""
-    B, H, D = cache.B, cache.H, cache.D
+    B, H, D, dev = cache.B, cache.H, cache.D, cache.device
     Hq = q.shape[1] if q.dim() > 1 else 0
-    _shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
+    if q.shape != (B, Hq, D) and q.shape != (B, Hq, 1, D):
+        _bad_shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
     n_keep = blocks.shape[-1] if blocks.dim() else 0
-    _shape(blocks, "blocks", (B, H, n_keep))
-    _shape(scores, "scores", (B, H, cache.Tmax // cache.G))
-    dev = cache.device
-    _check(load().kivi_block_select(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq,
-                                    _dev(blocks, torch.int32, "blocks", dev), n_keep,
-                                    _dev(scores, torch.float32, "scores", dev), _stream(stream, dev)),
-           "kivi_block_select")
+    if blocks.shape != (B, H, n_keep):
+        _bad_shape(blocks, "blocks", (B, H, n_keep))
+    if scores.shape != (B, H, cache.Tmax // cache.G):
+        _bad_shape(scores, "scores", (B, H, cache.Tmax // cache.G))
+    _call(load().kivi_block_select, "kivi_block_select", dev, C.byref(cache.desc),
+          _ptr(q, torch.float16, "q", dev), Hq, _ptr(blocks, torch.int32, "blocks", dev), n_keep,
+          _ptr(scores, torch.float32, "scores", dev), _raw_stream(stream, dev))
 
 
 def kivi_sparse_attention(cache, q: torch.Tensor, blocks: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
@@ -334,19 +358,19 @@ def kivi_sparse_attention(cache, q: torch.Tensor, blocks: torch.Tensor, out: tor
     """out fp32 [B, Hq, D] <- decode attention of q fp16 [B, Hq, D] (or
     [B, Hq, 1, D]) over the key groups blocks int32 [B, H, n_keep] lists and
     the fp16 residual; ws of at least kivi_attend_workspace_bytes(cache, Hq)."""
-    B, H, D = cache.B, cache.H, cache.D
+    B, H, D, dev = cache.B, cache.H, cache.D, cache.device
     Hq = q.shape[1] if q.dim() > 1 else 0
-    _shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
+    if q.shape != (B, Hq, D) and q.shape != (B, Hq, 1, D):
+        _bad_shape(q, "q", (B, Hq, D), (B, Hq, 1, D))
     n_keep = blocks.shape[-1] if blocks.dim() else 0
-    _shape(blocks, "blocks", (B, H, n_keep))
-    _shape(out, "out", (B, Hq, D), (B, Hq, 1, D))
-    sm = float(D ** -0.5) if sm_scale is None else float(sm_scale)
-    dev = cache.device
-    wp, wb = _ws(ws, dev)
-    _check(load().kivi_sparse_attention(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq, sm,
-                                        _dev(blocks, torch.int32, "blocks", dev), n_keep,
-                                        _dev(out, torch.float32, "out", dev), wp, wb, _stream(stream, dev)),
-           "kivi_sparse_attention")
+    if blocks.shape != (B, H, n_keep):
+        _bad_shape(blocks, "blocks", (B, H, n_keep))
+    if out.shape != (B, Hq, D) and out.shape != (B, Hq, 1, D):
+        _bad_shape(out, "out", (B, Hq, D), (B, Hq, 1, D))
+    _call(load().kivi_sparse_attention, "kivi_sparse_attention", dev, C.byref(cache.desc),
+          _ptr(q, torch.float16, "q", dev), Hq, D ** -0.5 if sm_scale is None else float(sm_scale),
+          _ptr(blocks, torch.int32, "blocks", dev), n_keep, _ptr(out, torch.float32, "out", dev),
+          _ptr(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(), _raw_stream(stream, dev))
 
 
 def kivi_tree_attention(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor,
@@ -358,24 +382,26 @@ def kivi_tree_attention(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     token i attends token j).  n_draft int32 [B]: tokens each sequence drafted
     (rows from there on keep their contents); ws of at least
     kivi_attend_workspace_bytes(cache, Hq, N)."""
-    B, H, D = cache.B, cache.H, cache.D
+    B, H, D, dev = cache.B, cache.H, cache.D, cache.device
     Hq, N = (q.shape[1], q.shape[2]) if q.dim() == 4 else (0, 0)
-    _shape(q, "q", (B, Hq, N, D))
-    _shape(k, "k", (B, H, N, D))
-    _shape(v, "v", (B, H, N, D))
-    _shape(mask, "mask", (B, N, (N + 63) // 64))
-    _shape(out, "out", (B, Hq, N, D))
-    dev = cache.device
-    if n_draft is not None:
-        _shape(n_draft, "n_draft", (B,))
-    sm = float(D ** -0.5) if sm_scale is None else float(sm_scale)
-    wp, wb = _ws(ws, dev)
-    _check(load().kivi_tree_attention(C.byref(cache.desc), _dev(q, torch.float16, "q", dev), Hq, N,
-                                      _dev(k, torch.float16, "k", dev), _dev(v, torch.float16, "v", dev),
-                                      _dev(mask, torch.int64, "mask", dev),
-                                      None if n_draft is None else _dev(n_draft, torch.int32, "n_draft", dev),
-                                      sm, _dev(out, torch.float32, "out", dev), wp, wb, _stream(stream, dev)),
-           "kivi_tree_attention")
+    if q.shape != (B, Hq, N, D):
+        _bad_shape(q, "q", (B, Hq, N, D))
+    if k.shape != (B, H, N, D):
+        _bad_shape(k, "k", (B, H, N, D))
+    if v.shape != (B, H, N, D):
+        _bad_shape(v, "v", (B, H, N, D))
+    if mask.shape != (B, N, (N + 63) // 64):
+        _bad_shape(mask, "mask", (B, N, (N + 63) // 64))
+    if out.shape != (B, Hq, N, D):
+        _bad_shape(out, "out", (B, Hq, N, D))
+    if n_draft is not None and n_draft.shape != (B,):
+        _bad_shape(n_draft, "n_draft", (B,))
+    _call(load().kivi_tree_attention, "kivi_tree_attention", dev, C.byref(cache.desc),
+          _ptr(q, torch.float16, "q", dev), Hq, N, _ptr(k, torch.float16, "k", dev),
+          _ptr(v, torch.float16, "v", dev), _ptr(mask, torch.int64, "mask", dev),
+          None if n_draft is None else _ptr(n_draft, torch.int32, "n_draft", dev),
+          D ** -0.5 if sm_scale is None else float(sm_scale), _ptr(out, torch.float32, "out", dev),
+          _ptr(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(), _raw_stream(stream, dev))
 
 
 def kivi_append_path(cache, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor, counts: torch.Tensor,
@@ -384,21 +410,23 @@ def kivi_append_path(cache, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor
     int32 [B]) of k, v fp16 [B, H, N, D] to every sequence.  A sequence with a
     bad count or path entry, or without room, is left as it was and status[0]
     set on the device (KIVI_EINVAL, KIVI_ECAPACITY)."""
-    B, H, D = cache.B, cache.H, cache.D
+    B, H, D, dev = cache.B, cache.H, cache.D, cache.device
     N = k.shape[2] if k.dim() == 4 else 0
-    _shape(k, "k", (B, H, N, D))
-    _shape(v, "v", (B, H, N, D))
+    if k.shape != (B, H, N, D):
+        _bad_shape(k, "k", (B, H, N, D))
+    if v.shape != (B, H, N, D):
+        _bad_shape(v, "v", (B, H, N, D))
     P = path.shape[-1] if path.dim() else 0
-    _shape(path, "path", (B, P))
-    _shape(counts, "counts", (B,))
+    if path.shape != (B, P):
+        _bad_shape(path, "path", (B, P))
+    if counts.shape != (B,):
+        _bad_shape(counts, "counts", (B,))
     if status.numel() < 1:
         raise ValueError("status must hold one int32")
-    dev = cache.device
-    _check(load().kivi_append_path(C.byref(cache.desc), _dev(k, torch.float16, "k", dev),
-                                   _dev(v, torch.float16, "v", dev), N, _dev(path, torch.int32, "path", dev), P,
-                                   _dev(counts, torch.int32, "counts", dev),
-                                   _dev(status, torch.int32, "status", dev), _stream(stream, dev)),
-           "kivi_append_path")
+    _call(load().kivi_append_path, "kivi_append_path", dev, C.byref(cache.desc), _ptr(k, torch.float16, "k", dev),
+          _ptr(v, torch.float16, "v", dev), N, _ptr(path, torch.int32, "path", dev), P,
+          _ptr(counts, torch.int32, "counts", dev), _ptr(status, torch.int32, "status", dev),
+          _raw_stream(stream, dev))
 
 
 def _payload_buf(t: torch.Tensor, name: str, device) -> int:

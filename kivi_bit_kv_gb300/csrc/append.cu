@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(128)
 append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int N,
                    const int32_t* __restrict__ path, int P, const int32_t* __restrict__ counts, int32_t* status)
 {
+    asm volatile("griddepcontrol.launch_dependents;");
     const size_t bh = blockIdx.x;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
     const int L = ld_checked(c.len + b);
@@ -202,7 +203,8 @@ append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t*
     }
 }
 
-// One warp per sequence: adds the tokens append_path_kernel appended.
+// One warp per sequence: adds the tokens append_path_kernel appended.  Its CTAs
+// start with that kernel's, which read `len`, and write once it has ended.
 __global__ void __launch_bounds__(128)
 advance_path_kernel(kivi_cache c, int N, const int32_t* __restrict__ path, int P,
                     const int32_t* __restrict__ counts)
@@ -212,7 +214,7 @@ advance_path_kernel(kivi_cache c, int N, const int32_t* __restrict__ path, int P
         return;
     const int L = ld_checked(c.len + b), n = ldg_checked(counts + b);
     const int st = path_status(c, L, n, path + (size_t)b * P, N, P);
-    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (st == KIVI_OK && (threadIdx.x & 31) == 0)
         st_checked(c.len + b, L + n);
 }
@@ -241,8 +243,19 @@ cudaError_t launch_append_path(const kivi_cache& c, const uint16_t* k, const uin
     case 4: launch_append_path_bk<4>(c, k, v, N, path, P, counts, status, s); break;
     default: launch_append_path_bk<8>(c, k, v, N, path, P, counts, status, s); break;
     }
-    advance_path_kernel<<<(c.B + 3) / 4, 128, 0, s>>>(c, N, path, P, counts);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((c.B + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, advance_path_kernel, c, N, path, P, counts);
 }
 
 #ifdef KIVI_CHECKS

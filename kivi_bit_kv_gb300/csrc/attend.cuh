@@ -1144,7 +1144,8 @@ cudaError_t attend_launch_rows(const kivi_cache& c, const AttendArgs& a, float* 
     if (pl.ns < 1)
         return cudaErrorInvalidConfiguration;
     const int smem = 1024 + C::O_RING + pl.ns * (pl.kst + pl.vst);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static int allowed[64];
+    cudaError_t e = allow_smem(kern, kAttSmem - C::STATIC, allowed);
     if (e != cudaSuccess)
         return e;
     const int N = cmin(C::CTAS * sm_count(), kAttMaxCTAs);

@@ -195,16 +195,28 @@ __device__ __forceinline__ void warp_values(const uint8_t* st, uint8_t* hat, int
         const int ck = (j + (lane >> SH)) & (NCH - 1);
         const uint4 v = *reinterpret_cast<const uint4*>(st + tok * ROW + ck * 16);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        constexpr int RUNS = CPC < 32 ? 1 : 2;  // runs of 16 channels that share statistics (G >= 32)
 #pragma unroll
-        for (int r = 0; r < CPC / 16; ++r) {  // runs of 16 channels
-            const int c0 = ck * CPC + 16 * r;
-            uint32_t y[BITS / 2], h[8];
+        for (int p = 0; p < CPC / (16 * RUNS); ++p) {
+            const int g = (ck * CPC + 32 * p) >> lgG;
+            const float sv = sc[g], zv = zr[g];
 #pragma unroll
-            for (int k = 0; k < BITS / 2; ++k)
-                y[k] = w[r * (BITS / 2) + k];
-            hat16<BITS>(y, sc[c0 >> lgG], zr[c0 >> lgG], h);
-            *reinterpret_cast<uint4*>(row + ((c0 * 2) ^ x)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + ((c0 * 2 + 16) ^ x)) = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int r = RUNS * p; r < RUNS * (p + 1); ++r) {
+                uint32_t y[BITS / 2], h[8];
+#pragma unroll
+                for (int k = 0; k < BITS / 2; ++k)
+                    y[k] = w[r * (BITS / 2) + k];
+                hat16<BITS>(y, sv, zv, h);
+                uint8_t* dst = row + ck * (CPC * 2);
+                if constexpr (CPC >= 64) {  // a chunk covers whole 128-byte lines: the swizzle stays inside them
+                    *reinterpret_cast<uint4*>(dst + ((32 * r) ^ x)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(dst + ((32 * r + 16) ^ x)) = make_uint4(h[4], h[5], h[6], h[7]);
+                } else {
+                    const int c0 = ck * (CPC * 2) + 32 * r;
+                    *reinterpret_cast<uint4*>(row + (c0 ^ x)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(row + ((c0 + 16) ^ x)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+            }
         }
     }
 }
@@ -569,25 +581,46 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 // blocks: token + 8 (lane / 16), channel chunk (lane / 8) % 2
                 const int tok = (lane & 7) + ((lane >> 4) << 3), ck = (lane >> 3) & 1;
                 const uint32_t at = smem_addr(hat) + tok * (2 * D), sw = (tok & 7) << 4;
+                // The unit's sums start at zero and are added to the row's with rounded
+                // additions: the tensor core truncates, and a chain through every unit
+                // of a long row would lose in one direction.  TG tiles at a time, so
+                // that their products do not wait for one another.
+                constexpr int TG = NT == 1 ? 4 : 2;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int t0 = 0; t0 < D / 16; t0 += TG) {
+                    float sum[TG][NT][4];
 #pragma unroll
-                    for (int t0 = 0; t0 < D / 16; t0 += 4) {  // four tiles: their products do not wait for one another
-                        uint32_t f[4][4];
+                    for (int t = 0; t < TG; ++t)
 #pragma unroll
-                        for (int t = 0; t < 4; ++t)
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                sum[t][nt][k] = 0.0f;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t f[TG][4];
+#pragma unroll
+                        for (int t = 0; t < TG; ++t)
                             ldsm_x4_t(f[t], at + m * (32 * D) + (((2 * (t0 + t) + ck) << 4) ^ sw));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                mma_f16(o[t0 + t][nt], f[t][0], f[t][1], f[t][2], f[t][3], ph[m][nt][0], ph[m][nt][1]);
+                            for (int t = 0; t < TG; ++t)
+                                mma_f16(sum[t][nt], f[t][0], f[t][1], f[t][2], f[t][3], ph[m][nt][0], ph[m][nt][1]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                mma_f16(o[t0 + t][nt], f[t][0], f[t][1], f[t][2], f[t][3], pl2[m][nt][0], pl2[m][nt][1]);
+                            for (int t = 0; t < TG; ++t)
+                                mma_f16(sum[t][nt], f[t][0], f[t][1], f[t][2], f[t][3], pl2[m][nt][0], pl2[m][nt][1]);
                     }
+#pragma unroll
+                    for (int t = 0; t < TG; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                o[t0 + t][nt][k] += sum[t][nt][k];
+                }
             }
             __syncwarp();  // V_hat has been read
         } else {  // a skipped unit: the next one's copies all the same
@@ -790,7 +823,8 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
     if (pl.warps < 1)
         return cudaErrorInvalidConfiguration;
     const int smem = pl.warps * pl.bytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static int allowed[64];
+    cudaError_t e = allow_smem(kern, kAttSmem - kStatic, allowed);
     if (e != cudaSuccess)
         return e;
     const int N = cmin(sm_count(), kAttMaxCTAs / 2);

@@ -12,6 +12,24 @@ namespace kivi {
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
+// Lets `kern` use `bytes` of dynamic shared memory; asks the runtime once per
+// device (`done`: a static of the launcher).  `bytes` is a constant of the
+// kernel, so that host threads that race ask for the same.
+template <class Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, int (&done)[64])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 64 && __atomic_load_n(&done[dev], __ATOMIC_RELAXED))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        __atomic_store_n(&done[dev], 1, __ATOMIC_RELAXED);
+    return e;
+}
+
 // Number of decode chunks (one CTA per KV head and chunk) that cover Tmax.
 int pv_chunks(const kivi_cache& c, int Hq);
 
