@@ -366,8 +366,8 @@ int32_t kivi_block_select(const kivi_cache* c, const uint16_t* q, int32_t Hq, in
     if (st != KIVI_OK || (st = check_heads(c, Hq)) != KIVI_OK || (st = check_ptr(q, "q")) != KIVI_OK ||
         (st = check_blocks(c, blocks, n_keep)) != KIVI_OK || (st = check_ptr(scores, "scores")) != KIVI_OK)
         return st;
-    // one CTA per (b, h) and 32 groups at most, in a 1-D grid
-    const long long ctas = (long long)c->B * c->H * ((c->Tmax / c->G + 31) / 32);
+    // one CTA per (b, h) and 128 groups or more, in a 1-D grid
+    const long long ctas = (long long)c->B * c->H * ((c->Tmax / c->G + 127) / 128);
     if (ctas >= (1ll << 31))
         return fail(KIVI_EINVAL, "%lld score CTAs; the grid holds fewer than 2^31", ctas);
     if ((st = check_current_device(c)) != KIVI_OK)

@@ -9,116 +9,162 @@
 // channels is pairwise over neighbours: inside a lane first (a lane holds
 // D / 32 neighbouring channels), then lane pairs 1, 2, 4, 8, 16 apart.
 //
-// Bound by the statistics' bytes (8 D a group).  A warp scores eight
-// neighbouring groups (four at D = 256), so that sixteen loads a lane are in
-// flight, and reduces the eight sums together: a lane keeps half of what it
-// holds at each of the first three exchanges, nine shuffles instead of forty.
+// Bound by the statistics' bytes (8 D a group).  A warp scores 512 / D
+// neighbouring groups at a time while the next ones' statistics are on their
+// way to its part of shared memory (cp.async: no lane reads what another
+// copied, so nothing waits at a barrier), and reduces their sums together: a lane keeps half of
+// what it holds at each of the first exchanges (four groups: six shuffles
+// instead of twenty).
 #include "kivi_device.cuh"
 #include "kivi_launch.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace kivi {
 
-constexpr int kScoreThreads = 256;
-// groups of a warp: sixteen or more 16-byte loads a lane in flight within 128
-// registers
-__host__ __device__ constexpr int score_groups(int D) { return D == 256 ? 4 : 8; }
-constexpr int kSelectThreads = 256;
-constexpr int kSelectKeys = 8;    // keys a thread keeps in registers
-static_assert(kSelectThreads == 256, "one histogram bin per thread");
+constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreStages = 3;     // a warp's ring of statistics
+constexpr int kScoreStage = 4096;   // bytes: the two statistics of score_groups(D) groups
+constexpr int kScoreRing = kScoreWarps * kScoreStages * kScoreStage;
+// groups of a warp at a time: 16 values of each statistic a lane
+__host__ __device__ constexpr int score_groups(int D) { return 512 / D; }
+
+// Threads that choose for one row, and the keys each keeps in registers.
+struct PickWarp { static constexpr int T = 32, K = 16; };
+struct PickCta { static constexpr int T = 256, K = 8; };
 
 __device__ __forceinline__ int cache_len(const kivi_cache& c, int b)
 {
     return min(max(ld_checked(c.len + b), 0), c.Tmax);
 }
 
+// cp_async16, or its 8-byte form.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const float* src)
+{
+    if constexpr (BYTES == 16) {
+        cp_async16(dst, src);
+    } else {
+        if (KIVI_IN_RANGE(src, BYTES))
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                         "l"(src), "n"(BYTES)
+                         : "memory");
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads)
-block_score_kernel(kivi_cache c, const uint16_t* __restrict__ q, int gq, float M, float* __restrict__ scores)
+block_score_kernel(kivi_cache c, const uint16_t* __restrict__ q, int gq, int iters, float M,
+                   float* __restrict__ scores)
 {
     constexpr int CPL = D / 32;  // channels per lane: 2, 4 or 8
     constexpr int V = CPL < 4 ? CPL : 4, NV = CPL / V;
     constexpr int NG = score_groups(D);
-    // q+ and q- of the heads
-    __shared__ float2 s_q[16 * D];
+    extern __shared__ __align__(16) uint8_t s_ring[];
+    float* s_q = reinterpret_cast<float*>(s_ring + kScoreRing);  // [gq][D]
     asm volatile("griddepcontrol.launch_dependents;");
     const int NB = c.Tmax / c.G, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int chunks = (NB + NG * (kScoreThreads / 32) - 1) / (NG * (kScoreThreads / 32));
+    const int per = iters * NG * kScoreWarps, chunks = (NB + per - 1) / per;
     const size_t bh = blockIdx.x / chunks;
     const int nb = quantized_tokens(cache_len(c, (int)(bh / c.H)), c.G, c.R) / c.G;
-    const int first = (int)(blockIdx.x % chunks) * NG * (kScoreThreads / 32);
+    const int first = (int)(blockIdx.x % chunks) * per, end = min(first + per, nb);
     if (first >= nb)
         return;
-    for (int i = threadIdx.x; i < gq * D; i += kScoreThreads) {
-        const float x = __half2float(__ushort_as_half(ldg_checked(q + bh * gq * D + i)));
-        s_q[i] = make_float2(fmaxf(x, 0.0f), fminf(x, 0.0f));
-    }
+    // lane's share of a vector: NV pieces of V channels, 32 lanes' pieces side by side
+    uint8_t* mine = s_ring + warp * kScoreStages * kScoreStage + lane * (4 * V);
+    constexpr int kPiece = 32 * 4 * V;
+    auto issue = [&](int it) {
+        const int g0 = first + (it * kScoreWarps + warp) * NG;
+        if (g0 < end) {
+            uint8_t* dst = mine + it % kScoreStages * kScoreStage;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+                const size_t at = (bh * NB + min(g0 + k, nb - 1)) * D + lane * CPL;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    copy_async<4 * V>(dst + (2 * k * NV + v) * kPiece, c.kzero + at + V * v);
+                    copy_async<4 * V>(dst + ((2 * k + 1) * NV + v) * kPiece, c.kscale + at + V * v);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int it = 0; it < kScoreStages - 1; ++it)
+        issue(it);
+    for (int i = threadIdx.x; i < gq * D; i += kScoreThreads)
+        s_q[i] = __half2float(__ushort_as_half(ldg_checked(q + bh * gq * D + i)));
     __syncthreads();
-    const int g0 = first + warp * NG;
-    if (g0 >= nb)
-        return;
-    float lo[NG][CPL], hi[NG][CPL];
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-        const size_t at = (bh * NB + min(g0 + k, nb - 1)) * D + lane * CPL;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if constexpr (V == 4) {
-                const float4 z = ld_nc_f4(c.kzero + at + 4 * v), s = ld_nc_f4(c.kscale + at + 4 * v);
-                lo[k][4 * v] = z.x, lo[k][4 * v + 1] = z.y, lo[k][4 * v + 2] = z.z, lo[k][4 * v + 3] = z.w;
-                hi[k][4 * v] = s.x, hi[k][4 * v + 1] = s.y, hi[k][4 * v + 2] = s.z, hi[k][4 * v + 3] = s.w;
-            } else {
-                const float2 z = ldg_checked(reinterpret_cast<const float2*>(c.kzero + at));
-                const float2 s = ldg_checked(reinterpret_cast<const float2*>(c.kscale + at));
-                lo[k][0] = z.x, lo[k][1] = z.y;
-                hi[k][0] = s.x, hi[k][1] = s.y;
-            }
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < NG; ++k)
-#pragma unroll
-        for (int i = 0; i < CPL; ++i)
-            hi[k][i] = __fadd_rn(lo[k][i], __fmul_rn(hi[k][i], M));
-    float best = 0.0f;
 #pragma unroll 1
-    for (int h = 0; h < gq; ++h) {
-        float2 x[CPL];
+    for (int it = 0;; ++it) {
+        const int now = first + (it * kScoreWarps + warp) * NG;
+        if (now >= end)
+            break;
+        issue(it + kScoreStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+        // a lane reads what it copied itself
+        const uint8_t* src = mine + it % kScoreStages * kScoreStage;
+        float l[NG][CPL], hi[NG][CPL];
 #pragma unroll
-        for (int i = 0; i < CPL; ++i)
-            x[i] = s_q[h * D + lane * CPL + i];
-        float t[NG];
+        for (int k = 0; k < NG; ++k)
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-            float y[CPL];
+            for (int v = 0; v < NV; ++v) {
+                using Vec = typename std::conditional<V == 4, float4, float2>::type;
+                const Vec z = *reinterpret_cast<const Vec*>(src + (2 * k * NV + v) * kPiece);
+                const Vec s = *reinterpret_cast<const Vec*>(src + ((2 * k + 1) * NV + v) * kPiece);
+                const float* zp = reinterpret_cast<const float*>(&z);
+                const float* sp = reinterpret_cast<const float*>(&s);
 #pragma unroll
-            for (int i = 0; i < CPL; ++i)
-                y[i] = __fmaf_rn(x[i].x, hi[k][i], __fmul_rn(x[i].y, lo[k][i]));
-#pragma unroll
-            for (int n = CPL / 2; n > 0; n /= 2)
-#pragma unroll
-                for (int i = 0; i < n; ++i)
-                    y[i] = __fadd_rn(y[2 * i], y[2 * i + 1]);
-            t[k] = y[0];
-        }
-        // the lane with the bit clear keeps the first half of the groups
-#pragma unroll
-        for (int o = 1, half = NG / 2; o < 32; o <<= 1, half /= 2) {
-            if (half == 0)
-                t[0] = __fadd_rn(t[0], __shfl_xor_sync(0xffffffffu, t[0], o));
-#pragma unroll
-            for (int k = 0; k < half; ++k) {
-                const float give = lane & o ? t[k] : t[k + half], keep = lane & o ? t[k + half] : t[k];
-                t[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                for (int i = 0; i < V; ++i) {
+                    l[k][V * v + i] = zp[i];
+                    hi[k][V * v + i] = __fadd_rn(zp[i], __fmul_rn(sp[i], M));
+                }
             }
-        }
-        best = h == 0 ? t[0] : fmaxf(best, t[0]);
-    }
-    int k = 0;  // the group that this lane holds
+        float best = 0.0f;
+#pragma unroll 1
+        for (int h = 0; h < gq; ++h) {
+            float pos[CPL], neg[CPL];
 #pragma unroll
-    for (int o = 1, half = NG / 2; half > 0; o <<= 1, half /= 2)
-        k += lane & o ? half : 0;
-    if (lane < NG && g0 + k < nb)
-        st_checked(scores + bh * NB + g0 + k, best);
+            for (int i = 0; i < CPL; ++i) {
+                const float x = s_q[h * D + lane * CPL + i];
+                pos[i] = fmaxf(x, 0.0f);
+                neg[i] = fminf(x, 0.0f);
+            }
+            float t[NG];
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+                float y[CPL];
+#pragma unroll
+                for (int i = 0; i < CPL; ++i)
+                    y[i] = __fmaf_rn(pos[i], hi[k][i], __fmul_rn(neg[i], l[k][i]));
+#pragma unroll
+                for (int n = CPL / 2; n > 0; n /= 2)
+#pragma unroll
+                    for (int i = 0; i < n; ++i)
+                        y[i] = __fadd_rn(y[2 * i], y[2 * i + 1]);
+                t[k] = y[0];
+            }
+            // the lane with the bit clear keeps the first half of the groups
+#pragma unroll
+            for (int o = 1, half = NG / 2; o < 32; o <<= 1, half /= 2) {
+                if (half == 0)
+                    t[0] = __fadd_rn(t[0], __shfl_xor_sync(0xffffffffu, t[0], o));
+#pragma unroll
+                for (int k = 0; k < half; ++k) {
+                    const float give = lane & o ? t[k] : t[k + half], keep = lane & o ? t[k + half] : t[k];
+                    t[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                }
+            }
+            best = h == 0 ? t[0] : fmaxf(best, t[0]);
+        }
+        int k = 0;  // the group that this lane holds
+#pragma unroll
+        for (int o = 1, half = NG / 2; half > 0; o <<= 1, half /= 2)
+            k += lane & o ? half : 0;
+        if (lane < NG && now + k < nb)
+            st_checked(scores + bh * NB + now + k, best);
+    }
 }
 
 // Order-preserving 32-bit key of a score: larger score, larger key; -0 counts
@@ -151,12 +197,14 @@ __device__ __forceinline__ void scan_words(uint32_t* w, int n)
 // One CTA per (b, h): a radix select finds the key of the n_keep-th largest
 // score in four passes of eight bits, then one ordered pass writes the indices
 // above it and the first of those equal to it.  Bound by latency: per pass a
-// histogram in shared memory and one warp's scan of it, with up to 2048 keys
-// in registers throughout (a longer row reads its scores again).
-__global__ void __launch_bounds__(kSelectThreads)
+// histogram in shared memory and one warp's scan of it, with up to T K keys in
+// registers throughout (a longer row reads its scores again).
+template <class P>
+__global__ void __launch_bounds__(P::T)
 block_pick_kernel(kivi_cache c, const float* __restrict__ scores, int32_t* __restrict__ blocks, int n_keep)
 {
-    constexpr int T = kSelectThreads, W = T / 32, K = kSelectKeys;
+    constexpr int T = P::T, W = T / 32, K = P::K;
+    static_assert(W * K <= 64, "scan_words takes 64 counters");
     __shared__ uint32_t hist[256];
     __shared__ uint32_t s_digit, s_need, s_base[2];
     __shared__ uint32_t s_eq[W * K], s_take[W * K];
@@ -185,7 +233,8 @@ block_pick_kernel(kivi_cache c, const float* __restrict__ scores, int32_t* __res
     uint32_t prefix = 0, need = (uint32_t)m;  // need of the keys that start with prefix
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
+        for (int i = tid; i < 256; i += T)
+            hist[i] = 0;
         __syncthreads();
         auto count = [&](uint32_t x) {
             if (shift == 24 || (x >> (shift + 8)) == prefix)
@@ -284,34 +333,59 @@ block_pick_kernel(kivi_cache c, const float* __restrict__ scores, int32_t* __res
     }
 }
 
+template <int D>
+static cudaError_t launch_score(const kivi_cache& c, dim3 grid, int smem, const uint16_t* q, int gq, int iters,
+                                float M, float* scores, cudaStream_t s)
+{
+    static int allowed[64];
+    const cudaError_t e = allow_smem(block_score_kernel<D>, kScoreRing + 16 * D * 4, allowed);
+    if (e != cudaSuccess)
+        return e;
+    block_score_kernel<D><<<grid, kScoreThreads, smem, s>>>(c, q, gq, iters, M, scores);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_block_select(const kivi_cache& c, const uint16_t* q, int Hq, int32_t* blocks, int n_keep,
                                 float* scores, cudaStream_t s)
 {
     const int NB = c.Tmax / c.G, BH = c.B * c.H;
     KIVI_SET_CHECK_RANGES(c, s, {{q, (size_t)c.B * Hq * c.D * 2}, {blocks, (size_t)BH * n_keep * 4},
                                  {scores, (size_t)BH * NB * 4}});
-    const int per = score_groups(c.D) * (kScoreThreads / 32);
-    const dim3 grid((unsigned)BH * (unsigned)((NB + per - 1) / per));
+    // A row's groups go to equal chunks: as many as keep two CTAs an SM busy once,
+    // with eight steps of a warp at most.
+    const int units = (NB + score_groups(c.D) * kScoreWarps - 1) / (score_groups(c.D) * kScoreWarps);
+    const long long waves = ((long long)BH * units + 2 * sm_count() - 1) / (2 * sm_count());
+    const int most = (int)std::min(8ll, waves), iters = (units + (units + most - 1) / most - 1) / ((units + most - 1) / most);
+    const dim3 grid((unsigned)BH * (unsigned)((units + iters - 1) / iters));
+    const int gq = Hq / c.H, smem = kScoreRing + gq * c.D * 4;
     const float M = (float)((1 << c.bits_k) - 1);
+    cudaError_t e;
     switch (c.D) {
-    case 64: block_score_kernel<64><<<grid, kScoreThreads, 0, s>>>(c, q, Hq / c.H, M, scores); break;
-    case 128: block_score_kernel<128><<<grid, kScoreThreads, 0, s>>>(c, q, Hq / c.H, M, scores); break;
-    default: block_score_kernel<256><<<grid, kScoreThreads, 0, s>>>(c, q, Hq / c.H, M, scores); break;
+    case 64: e = launch_score<64>(c, grid, smem, q, gq, iters, M, scores, s); break;
+    case 128: e = launch_score<128>(c, grid, smem, q, gq, iters, M, scores, s); break;
+    default: e = launch_score<256>(c, grid, smem, q, gq, iters, M, scores, s); break;
     }
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     // the choice's CTAs are scheduled while the scores drain
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(BH);
-    cfg.blockDim = dim3(kSelectThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_pick_kernel, c, (const float*)scores, blocks, n_keep);
+    // A warp's registers hold a row of up to 512 groups.  With more rows than the
+    // CTAs of one wave a warp a row takes less of the machine (2048 rows: 14
+    // against 23 us), with fewer a CTA a row is sooner done (4 rows: 8.4 against
+    // 6.8 us).
+    if (NB <= PickWarp::T * PickWarp::K && BH > 4 * sm_count()) {
+        cfg.blockDim = dim3(PickWarp::T);
+        return cudaLaunchKernelEx(&cfg, block_pick_kernel<PickWarp>, c, (const float*)scores, blocks, n_keep);
+    }
+    cfg.blockDim = dim3(PickCta::T);
+    return cudaLaunchKernelEx(&cfg, block_pick_kernel<PickCta>, c, (const float*)scores, blocks, n_keep);
 }
 
 #ifdef KIVI_CHECKS
