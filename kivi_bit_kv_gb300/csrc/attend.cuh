@@ -168,6 +168,45 @@ __device__ __forceinline__ bool group_any(int id, bool x)
                  : "memory");
     return r != 0;
 }
+// A row's reference before its first token: below every logit, and finite, so
+// that a logit of -inf less it is -inf.
+constexpr float kAttNoRef = -3e38f;
+
+// 2^x, 0 below 2^-126 (a weight that small is nothing beside the largest, which
+// is 1 or more).
+__device__ __forceinline__ float ex2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two rounded operations in one instruction: x += y, x -= y, x *= f.
+__device__ __forceinline__ void put_pair(float* x, float2 r)
+{
+    x[0] = r.x;
+    x[1] = r.y;
+}
+__device__ __forceinline__ void add_pair(float* x, const float* y)
+{
+    put_pair(x, __fadd2_rn(make_float2(x[0], x[1]), make_float2(y[0], y[1])));
+}
+__device__ __forceinline__ void sub_pair(float* x, const float* y)
+{
+    put_pair(x, __ffma2_rn(make_float2(y[0], y[1]), make_float2(-1.0f, -1.0f), make_float2(x[0], x[1])));
+}
+__device__ __forceinline__ void mul_pair(float* x, float f)
+{
+    put_pair(x, __fmul2_rn(make_float2(x[0], x[1]), make_float2(f, f)));
+}
+// p = hi + lo as two fp16 pairs: the upper 11 bits, and what is left of them.
+__device__ __forceinline__ void split_pair(float* p, uint32_t& hi, uint32_t& lo)
+{
+    const float h[2] = {__uint_as_float(__float_as_uint(p[0]) & 0xFFFFE000u),
+                        __uint_as_float(__float_as_uint(p[1]) & 0xFFFFE000u)};
+    hi = h2_bits(__floats2half2_rn(h[0], h[1]));
+    sub_pair(p, h);
+    lo = h2_bits(__floats2half2_rn(p[0], p[1]));
+}
 // Waits for the phase of parity `parity` of mbarrier b; false, with the abort
 // flag set and the timeout recorded in *status (unless null), if it has not
 // completed within kAttWaitTries attempts (some four microseconds each) or *abort
@@ -879,7 +918,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     if constexpr (C::REG_REF)
-                        ref[k] = -INFINITY;
+                        ref[k] = kAttNoRef;
                     l[k] = 0.0f;
 #pragma unroll
                     for (int h = 0; h < MH; ++h)
@@ -888,7 +927,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 if constexpr (!C::REG_REF) {
                     named_bar(3 + wg, 128);  // the previous row tile's are no longer read
                     if (qd == 0)
-                        s_ref[wg][lane % NC] = -INFINITY;
+                        s_ref[wg][lane % NC] = kAttNoRef;
                     named_bar(3 + wg, 128);
                 }
             }
@@ -925,20 +964,18 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 tc_ld(y, src + k0);
                 tc_wait_ld(y);
 #pragma unroll
-                for (int k = 0; k < CH; ++k)
-                    y[k] = __fmul_rn(y[k], sl2);
+                for (int k = 0; k < CH; k += 2)
+                    mul_pair(y + k, sl2);
                 if constexpr (C::REG_REF) {
 #pragma unroll
-                    for (int k = 0; k < CH; ++k)
-                        y[k] -= ref[k0 + k];
+                    for (int k = 0; k < CH; k += 2)
+                        sub_pair(y + k, ref + k0 + k);
                 } else {
 #pragma unroll
                     for (int k = 0; k < CH; k += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(&s_ref[wg][k0 + k]);
-                        y[k] -= f.x;
-                        y[k + 1] -= f.y;
-                        y[k + 2] -= f.z;
-                        y[k + 3] -= f.w;
+                        sub_pair(y + k, &f.x);
+                        sub_pair(y + k + 2, &f.z);
                     }
                 }
                 apply_mask(k0);
@@ -962,8 +999,8 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                     tc_ld(y, src + k0);
                     tc_wait_ld(y);
 #pragma unroll
-                    for (int k = 0; k < CH; ++k)
-                        y[k] = __fmul_rn(y[k], sl2);
+                    for (int k = 0; k < CH; k += 2)
+                        mul_pair(y + k, sl2);
                     apply_mask(k0);
 #pragma unroll
                     for (int k = 0; k < CH; ++k) {
@@ -979,7 +1016,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 const float m = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
                 // a maximum beyond 2^20 is its own reference: 13 would be lost in it
                 const float next = fmaxf(old, fabsf(m) < 1048576.0f ? m - kAttShift : m);
-                const float alpha = next == old ? 1.0f : ex2(old - next);
+                const float alpha = next == old ? 1.0f : ex2_ftz(old - next);
                 if constexpr (!C::REG_REF) {
                     if (qd == 0)
                         s_ref[wg][lane % NC] = next;  // every warp has read the old one
@@ -1005,10 +1042,10 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 uint32_t hi[CH / 2], lo[CH / 2];
 #pragma unroll
                 for (int k = 0; k < CH; k += 2) {
-                    const float p0 = ex2(y[k]), p1 = ex2(y[k + 1]);
-                    l[k0 + k] += p0;
-                    l[k0 + k + 1] += p1;
-                    split_hi_lo(p0, p1, hi[k / 2], lo[k / 2]);
+                    y[k] = ex2_ftz(y[k]);
+                    y[k + 1] = ex2_ftz(y[k + 1]);
+                    add_pair(l + k0 + k, y + k);
+                    split_pair(y + k, hi[k / 2], lo[k / 2]);
                 }
                 const int r0 = wg * NC + k0;
                 if constexpr (NC < 8) {  // half a 16-byte chunk of each term
@@ -1055,14 +1092,14 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                         tc_wait_ld(y);
                         tc_wait_ld(z);
 #pragma unroll
-                        for (int k = 0; k < OC; ++k)
-                            y[k] += z[k];
+                        for (int k = 0; k < OC; k += 2)
+                            add_pair(y + k, z + k);
                     } else {
                         tc_wait_ld(y);
                     }
 #pragma unroll
-                    for (int k = 0; k < OC; ++k)
-                        o[h][k0 + k] += y[k];
+                    for (int k = 0; k < OC; k += 2)
+                        add_pair(o[h] + k0 + k, y + k);
                 }
             if (__builtin_expect(d.last, 0)) {
                 finish(i);
@@ -1105,14 +1142,12 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
         const int r = blockIdx.y * kAttCombineRows + e / D, d = e % D, row = rt * NR + r;
         if (row >= pl.M || row % a.N >= nd)
             continue;
-        float M = -INFINITY, L = 0.0f, o = 0.0f;
+        float M = kAttNoRef, L = 0.0f, o = 0.0f;
 #pragma unroll 1
         for (int k = i; k <= last; ++k) {
             const float* p = att_part(ws, D, NR, k, k == i);
             const float m = p[(size_t)NR * D + r], l = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
-            if (m == -INFINITY)
-                continue;
-            const float Mn = fmaxf(M, m), f = ex2(M - Mn), g = ex2(m - Mn);
+            const float Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
             L = L * f + l * g;
             o = o * f + x * g;
             M = Mn;

@@ -417,7 +417,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 #pragma unroll
             for (int k = 0; k < NCOL; ++k) {
                 l[k] = 0.0f;
-                ref[k] = -INFINITY;
+                ref[k] = kAttNoRef;
             }
 #pragma unroll
             for (int m = 0; m < D / 16; ++m)
@@ -490,8 +490,8 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s[m][nt][k] = __fmul_rn(s[m][nt][k], sl2);
+                    for (int k = 0; k < 4; k += 2)
+                        mul_pair(s[m][nt] + k, sl2);
             const int f0 = (w.j - w.s.nu) * 32;
             if (__builtin_expect(!quant && f0 + 32 > w.s.res, 0)) {
 #pragma unroll
@@ -518,8 +518,11 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top = fmaxf(top, s[m][nt][k] - ref[2 * nt + (k & 1)]);
+                    for (int k = 0; k < 4; k += 2) {
+                        float y[2] = {s[m][nt][k], s[m][nt][k + 1]};
+                        sub_pair(y, ref + 2 * nt);
+                        top = fmaxf(top, fmaxf(y[0], y[1]));
+                    }
             if (__builtin_expect(__any_sync(0xffffffffu, top > kAttLimit), 0)) {
                 // the references move to the rows' maxima so far
 #pragma unroll
@@ -532,7 +535,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
                         const float old = ref[2 * nt + e];
                         const float next = fmaxf(old, fabsf(m) < 1048576.0f ? m - kAttShift : m);
-                        const float alpha = next == old ? 1.0f : ex2(old - next);
+                        const float alpha = next == old ? 1.0f : ex2_ftz(old - next);
                         ref[2 * nt + e] = next;
                         l[2 * nt + e] *= alpha;
 #pragma unroll
@@ -550,15 +553,13 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float r0 = ref[2 * nt], r1 = ref[2 * nt + 1];
-                        const float y0 = s[m][nt][2 * hf], y1 = s[m][nt][2 * hf + 1];
-                        // a row without a token yet has ref = -inf and no logit above it
-                        const float p0 = y0 == -INFINITY ? 0.0f : ex2(y0 - r0);
-                        const float p1 = y1 == -INFINITY ? 0.0f : ex2(y1 - r1);
-                        l[2 * nt] += p0;
-                        l[2 * nt + 1] += p1;
+                        float p[2] = {s[m][nt][2 * hf], s[m][nt][2 * hf + 1]};
+                        sub_pair(p, ref + 2 * nt);
+                        p[0] = ex2_ftz(p[0]);
+                        p[1] = ex2_ftz(p[1]);
+                        add_pair(l + 2 * nt, p);
                         uint32_t hi, lo;
-                        split_hi_lo(p0, p1, hi, lo);
+                        split_pair(p, hi, lo);
                         ph[m][nt][hf] = mov_trans(hi);
                         pl2[m][nt][hf] = mov_trans(lo);
                     }
@@ -585,41 +586,38 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 // additions: the tensor core truncates, and a chain through every unit
                 // of a long row would lose in one direction.  TG tiles at a time, so
                 // that their products do not wait for one another.
-                constexpr int TG = NT == 1 ? 4 : 2;
+                constexpr int TG = 2;
 #pragma unroll
                 for (int t0 = 0; t0 < D / 16; t0 += TG) {
-                    float sum[TG][NT][4];
+                    uint32_t f[2][TG][4];
 #pragma unroll
-                    for (int t = 0; t < TG; ++t)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                sum[t][nt][k] = 0.0f;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t f[TG][4];
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int t = 0; t < TG; ++t)
-                            ldsm_x4_t(f[t], at + m * (32 * D) + (((2 * (t0 + t) + ck) << 4) ^ sw));
+                            ldsm_x4_t(f[m][t], at + m * (32 * D) + (((2 * (t0 + t) + ck) << 4) ^ sw));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float sum[TG][4];
 #pragma unroll
-                            for (int t = 0; t < TG; ++t)
-                                mma_f16(sum[t][nt], f[t][0], f[t][1], f[t][2], f[t][3], ph[m][nt][0], ph[m][nt][1]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int t = 0; t < TG; ++t)
-                                mma_f16(sum[t][nt], f[t][0], f[t][1], f[t][2], f[t][3], pl2[m][nt][0], pl2[m][nt][1]);
-                    }
-#pragma unroll
-                    for (int t = 0; t < TG; ++t)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int t = 0; t < TG; ++t)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                o[t0 + t][nt][k] += sum[t][nt][k];
+                                sum[t][k] = 0.0f;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                            for (int t = 0; t < TG; ++t)
+                                mma_f16(sum[t], f[m][t][0], f[m][t][1], f[m][t][2], f[m][t][3], ph[m][nt][0], ph[m][nt][1]);
+#pragma unroll
+                            for (int t = 0; t < TG; ++t)
+                                mma_f16(sum[t], f[m][t][0], f[m][t][1], f[m][t][2], f[m][t][3], pl2[m][nt][0], pl2[m][nt][1]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < TG; ++t)
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+                                add_pair(o[t0 + t][nt] + k, sum[t] + k);
+                    }
                 }
             }
             __syncwarp();  // V_hat has been read
@@ -743,14 +741,14 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
             float L = 0.0f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float wk = m[k] == -INFINITY ? 0.0f : ex2(m[k] - mx);
+                const float wk = m[k] == -INFINITY ? 0.0f : ex2_ftz(m[k] - mx);
                 s_w[r][lane + 32 * k] = wk;
                 L = fmaf(l[k], wk, L);
             }
 #pragma unroll
             for (int e = 16; e > 0; e >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, e);
-            const float f = old == mx ? 1.0f : ex2(old - mx);
+            const float f = old == mx ? 1.0f : ex2_ftz(old - mx);
             if (lane == 0) {
                 s_l[r] = s_l[r] * f + L;
                 s_m[r] = mx;
