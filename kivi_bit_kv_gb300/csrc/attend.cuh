@@ -17,17 +17,16 @@
 // in registers, so no long chain of tensor-core additions builds up.
 //
 // Tokens lie on the M axis (TMEM lanes) of both products and rows on the N
-// axis, so one row costs as little as one column: a decode step (one to
-// sixteen rows) and a verified tree (up to 128 rows per tile) run the same
-// code.  What a tile costs whatever the rows is rebuilding 2 x 128 x D fp16
-// operands from codes.
+// axis, so that a row costs one column and a tile has as many as there are (32,
+// 64 or 128; attend_warp.cuh serves fewer than 17).  What a tile costs whatever
+// the rows is rebuilding 2 x 128 x D fp16 operands from codes.
 //
-// Work.  One CTA per SM takes a contiguous range of the tiles of all row
-// tiles in order; a row tile cut by a range boundary leaves partial (o, m, l)
+// Work.  A CTA (one or two per SM) takes a contiguous range of the tiles of all
+// row tiles in order; a row tile cut by a range boundary leaves partial (o, m, l)
 // in the workspace, merged by attend_combine_kernel.  The split and every
 // sum's order depend only on sizes and lengths.
 //
-// Roles.  Sixteen worker warps share every step of a tile; two copy warps bring
+// Roles.  Eight or sixteen worker warps share every step of a tile; two copy warps bring
 // the packed codes and statistics of keys and values into rings of stages, and
 // one warp issues the products.  Per tile i the workers
 //     turn S(i) into P(i);        barrier, O(i) = V P is issued;
@@ -35,10 +34,11 @@
 //     add O(i) to the running output and, at a row's end, store it;
 //     rebuild the values of i + 1;
 // so both products run under the workers' arithmetic.  All workers run the same
-// code at the same time on purpose: with a warpgroup per step, every step off
-// the others' critical path, the kernel was 40 % slower -- each group fetched
-// its own instruction stream once per tile, and instruction fetch, not the
-// arithmetic, set the pace.  Worker warp w reads TMEM lanes 32 (w % 4) .. + 31
+// code at the same time on purpose: with a warpgroup per step (475 us for 8
+// rows of an int4 prefix, against 263) each group fetched its own instruction
+// stream once per tile, and instruction fetch, not the arithmetic, set the pace.
+// The widths are template arguments and the cold paths are functions for the
+// same reason.  Worker warp w reads TMEM lanes 32 (w % 4) .. + 31
 // (tokens, later channels) and the NC rows w / 4 of the tile.
 //
 // The softmax keeps one reference maximum per row and does not move it while
@@ -57,6 +57,13 @@
 // flag and records KIVI_ETIMEOUT in the workspace's status word; the CTA then
 // runs through without waiting, waits (bounded) for its copies and products,
 // frees its TMEM and ends.
+//
+// Measured: 128 query rows over four int2 contexts of 32768 tokens and eight KV
+// heads, D = 128: 296 us, 225 TFLOP/s of the two products (66.6 GFLOP) and 139
+// MB read once.  The chain of steps between barriers bounds it: the
+// schedulers issue in 56 % of the cycles, 35 instructions per weight, of which
+// six rebuild the operands; the tensor cores are busy 17 % of the time and DRAM
+// 7 %.
 #pragma once
 
 #include "attend_plan.h"
@@ -105,12 +112,6 @@ __device__ __forceinline__ uint32_t elect_lane()
 }
 // N columns of this thread's TMEM lane; the values are there after tc_wait_ld,
 // which names them so that no use can be scheduled before it.
-__device__ __forceinline__ void tc_ld(float (&r)[4], uint32_t a)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-                 : "r"(a));
-}
 __device__ __forceinline__ void tc_ld(float (&r)[8], uint32_t a)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -666,57 +667,57 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
             const unsigned mask = __ballot_sync(0xffffffffu, go);
 #pragma unroll 1
             for (int u0 = 0; u0 < 4; u0 += pl.su) {
-            if (round > 0 && !__all_sync(0xffffffffu, wait(&s_empty[which][slot], round - 1))) {
-                alive = false;
-                break;
-            }
-            uint64_t* bar = &s_full[which][slot];
-            const unsigned pmask = mask >> u0 & ((1u << pl.su) - 1);
-            if (lane == 0) {
-                if (which == 0 && u0 == 0) {
-                AttDesc& d = s_desc[i & (kAttDescs - 1)];
-                d.b = w.b;
-                d.rr = w.rr;
-                d.v0 = v0;
-                d.nuq = nuq;
-                d.f0 = v0 - w.s.nq;
-                d.Tq = w.s.Tq;
-                d.res = w.s.len - w.s.Tq;
-                d.nd = w.s.nd;
-                d.tail = w.j == w.s.nt - 1;
-                d.mid = starts_mid && w.b == b0 && w.rr == rr0;
-                d.first = w.j == 0 || i == 0;
-                d.last = d.tail || i == n - 1;
-                d.umask = mask;
-                if (__builtin_expect(i == n - 1 && !d.tail && !d.mid, 0)) {
-                    // the row tile starts in this range and its last tile, end - 1, is in range
-                    // `last`: the first with total (last + 1) / count >= end
-                    const long long end = s_range[1] + (w.s.nt - 1 - w.j);
-                    cut[1] = w.b;
-                    cut[2] = w.rr;
-                    cut[3] = (int)((end * s_range[3] + s_range[2] - 1) / s_range[2] - 1);
-                    cut[0] = 1;
+                if (round > 0 && !__all_sync(0xffffffffu, wait(&s_empty[which][slot], round - 1))) {
+                    alive = false;
+                    break;
                 }
+                uint64_t* bar = &s_full[which][slot];
+                const unsigned pmask = mask >> u0 & ((1u << pl.su) - 1);
+                if (lane == 0) {
+                    if (which == 0 && u0 == 0) {
+                        AttDesc& d = s_desc[i & (kAttDescs - 1)];
+                        d.b = w.b;
+                        d.rr = w.rr;
+                        d.v0 = v0;
+                        d.nuq = nuq;
+                        d.f0 = v0 - w.s.nq;
+                        d.Tq = w.s.Tq;
+                        d.res = w.s.len - w.s.Tq;
+                        d.nd = w.s.nd;
+                        d.tail = w.j == w.s.nt - 1;
+                        d.mid = starts_mid && w.b == b0 && w.rr == rr0;
+                        d.first = w.j == 0 || i == 0;
+                        d.last = d.tail || i == n - 1;
+                        d.umask = mask;
+                        if (__builtin_expect(i == n - 1 && !d.tail && !d.mid, 0)) {
+                            // the row tile starts in this range and its last tile, end - 1, is in range
+                            // `last`: the first with total (last + 1) / count >= end
+                            const long long end = s_range[1] + (w.s.nt - 1 - w.j);
+                            cut[1] = w.b;
+                            cut[2] = w.rr;
+                            cut[3] = (int)((end * s_range[3] + s_range[2] - 1) / s_range[2] - 1);
+                            cut[0] = 1;
+                        }
+                    }
+                    mbar_arrive_tx(bar, __popc(pmask) * (code + 2 * stat));
                 }
-                mbar_arrive_tx(bar, __popc(pmask) * (code + 2 * stat));
-            }
-            __syncwarp();
-            const int u = lane - u0;  // unit of the stage
-            if (go && u >= 0 && u < pl.su) {
-                const uint8_t* src = codes + (bh * (c.Tmax >> 5) + (t0 >> 5)) * code;
-                const size_t so = (bh * (c.Tmax >> lgs) + (t0 >> lgs)) * stat;
-                uint8_t* d = ring + slot * stage;
-                if (KIVI_IN_RANGE(src, code) && KIVI_IN_RANGE(scales + so, stat) && KIVI_IN_RANGE(zeros + so, stat)) {
-                    bulk_g2s(d + u * code, src, code, bar);
-                    bulk_g2s(d + pl.su * code + u * stat, scales + so, stat, bar);
-                    bulk_g2s(d + pl.su * (code + stat) + u * stat, zeros + so, stat, bar);
+                __syncwarp();
+                const int u = lane - u0;  // unit of the stage
+                if (go && u >= 0 && u < pl.su) {
+                    const uint8_t* src = codes + (bh * (c.Tmax >> 5) + (t0 >> 5)) * code;
+                    const size_t so = (bh * (c.Tmax >> lgs) + (t0 >> lgs)) * stat;
+                    uint8_t* d = ring + slot * stage;
+                    if (KIVI_IN_RANGE(src, code) && KIVI_IN_RANGE(scales + so, stat) && KIVI_IN_RANGE(zeros + so, stat)) {
+                        bulk_g2s(d + u * code, src, code, bar);
+                        bulk_g2s(d + pl.su * code + u * stat, scales + so, stat, bar);
+                        bulk_g2s(d + pl.su * (code + stat) + u * stat, zeros + so, stat, bar);
+                    }
                 }
-            }
-            ++sent;
-            if (++slot == pl.ns) {
-                slot = 0;
-                ++round;
-            }
+                ++sent;
+                if (++slot == pl.ns) {
+                    slot = 0;
+                    ++round;
+                }
             }
             if (!alive)
                 break;
@@ -889,8 +890,8 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 dst = piece + wg * NC * D;
                 const float rf = my_ref();
                 if (qd == 0 && lane < NC) {
-                    piece[(size_t)NR * D + wg * NC + lane] = rf;
-                    piece[(size_t)NR * D + NR + wg * NC + lane] = L;
+                    st_checked(piece + (size_t)NR * D + wg * NC + lane, rf);
+                    st_checked(piece + (size_t)NR * D + NR + wg * NC + lane, L);
                 }
             }
             uint32_t rows = __ballot_sync(0xffffffffu, mine);
@@ -903,7 +904,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 if ((rows >> k) & 1u)
 #pragma unroll
                     for (int x = 0; x < MH; ++x)
-                        dst[k * D + 128 * x] = o[x][k] * f;
+                        st_checked(dst + k * D + 128 * x, o[x][k] * f);
             }
         };
 
@@ -911,148 +912,143 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
         for (int i = -2; i < n; ++i) {  // -2 and -1: the keys of tiles 0 and 1, the values of 0
             const AttDesc& d = s_desc[i & (kAttDescs - 1)];
             if (i >= 0) {
-            if (i + 1 >= n)  // else it was waited for before the keys of tile i + 1
-                wait(&s_sdone[i & 1], i >> 1);
-            tc_fence_after();
-            if (__builtin_expect(d.first, 0)) {
+                if (i + 1 >= n)  // else it was waited for before the keys of tile i + 1
+                    wait(&s_sdone[i & 1], i >> 1);
+                tc_fence_after();
+                if (__builtin_expect(d.first, 0)) {
 #pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    if constexpr (C::REG_REF)
-                        ref[k] = kAttNoRef;
-                    l[k] = 0.0f;
+                    for (int k = 0; k < NC; ++k) {
+                        if constexpr (C::REG_REF)
+                            ref[k] = kAttNoRef;
+                        l[k] = 0.0f;
 #pragma unroll
-                    for (int h = 0; h < MH; ++h)
-                        o[h][k] = 0.0f;
-                }
-                if constexpr (!C::REG_REF) {
-                    named_bar(3 + wg, 128);  // the previous row tile's are no longer read
-                    if (qd == 0)
-                        s_ref[wg][lane % NC] = kAttNoRef;
-                    named_bar(3 + wg, 128);
-                }
-            }
-            // this warp's tokens: a quantized unit, or fp16 tokens
-            const bool quant = qd < d.nuq;
-            const bool skip = quant && !((d.umask >> qd) & 1u);
-            const int j = d.f0 + 32 * qd + lane - d.res;  // draft, at or past 0
-            const bool masked = skip || (!quant && j >= 0);
-            uint32_t sees = 0u;                           // rows (bits) that attend this lane's token
-            if (__builtin_expect(masked && !skip && j < d.nd, 0)) {
-                const uint64_t* mw = a.mask + (size_t)d.b * a.N * W + (j >> 6);
-                int row = ((d.rr % pl.RT) * NR + wg * NC) % a.N;
-#pragma unroll 2
-                for (int k = 0; k < NC; ++k) {
-                    if (row < d.nd)
-                        sees |= (uint32_t)((ldg_checked(mw + (size_t)row * W) >> (j & 63)) & 1) << k;
-                    if (++row == a.N)
-                        row = 0;
-                }
-            }
-            __syncwarp();
-            const uint32_t src = tm + C::TM_S + (i & 1) * NR + wg * NC + lanes;
-            float y[CH];
-            // -inf where the row does not attend the lane's token
-            auto apply_mask = [&](int k0) {
-                if (__builtin_expect(masked, 0)) {
-#pragma unroll
-                    for (int k = 0; k < CH; ++k)
-                        y[k] = (sees >> (k0 + k)) & 1u ? y[k] : -INFINITY;
-                }
-                __syncwarp();
-            };
-            auto exponents = [&](int k0) {
-                tc_ld(y, src + k0);
-                tc_wait_ld(y);
-#pragma unroll
-                for (int k = 0; k < CH; k += 2)
-                    mul_pair(y + k, sl2);
-                if constexpr (C::REG_REF) {
-#pragma unroll
-                    for (int k = 0; k < CH; k += 2)
-                        sub_pair(y + k, ref + k0 + k);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < CH; k += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&s_ref[wg][k0 + k]);
-                        sub_pair(y + k, &f.x);
-                        sub_pair(y + k + 2, &f.z);
+                        for (int h = 0; h < MH; ++h)
+                            o[h][k] = 0.0f;
+                    }
+                    if constexpr (!C::REG_REF) {
+                        named_bar(3 + wg, 128);  // the previous row tile's are no longer read
+                        if (qd == 0)
+                            s_ref[wg][lane % NC] = kAttNoRef;
+                        named_bar(3 + wg, 128);
                     }
                 }
-                apply_mask(k0);
-            };
-            // the second time round, after the references moved, no weight passes the limit
-#pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += CH) {
-                    exponents(k0);
-#pragma unroll
-                    for (int k = 0; k < CH; ++k)
-                        top = fmaxf(top, y[k]);
+                // this warp's tokens: a quantized unit, or fp16 tokens
+                const bool quant = qd < d.nuq;
+                const bool skip = quant && !((d.umask >> qd) & 1u);
+                const int j = d.f0 + 32 * qd + lane - d.res;  // draft, at or past 0
+                const bool masked = skip || (!quant && j >= 0);
+                uint32_t sees = 0u;                           // rows (bits) that attend this lane's token
+                if (__builtin_expect(masked && !skip && j < d.nd, 0)) {
+                    const uint64_t* mw = a.mask + (size_t)d.b * a.N * W + (j >> 6);
+                    int row = ((d.rr % pl.RT) * NR + wg * NC) % a.N;
+#pragma unroll 2
+                    for (int k = 0; k < NC; ++k) {
+                        if (row < d.nd)
+                            sees |= (uint32_t)((ldg_checked(mw + (size_t)row * W) >> (j & 63)) & 1) << k;
+                        if (++row == a.N)
+                            row = 0;
+                    }
                 }
-                if (__builtin_expect(pass == 1 || !group_any(3 + wg, top > kAttLimit), 1))
-                    break;
-                float mine = -INFINITY;  // the warp's largest logit of row `lane`
+                __syncwarp();
+                const uint32_t src = tm + C::TM_S + (i & 1) * NR + wg * NC + lanes;
+                float y[CH];
+                // -inf where the row does not attend the lane's token
+                auto apply_mask = [&](int k0) {
+                    if (__builtin_expect(masked, 0)) {
 #pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += CH) {
+                        for (int k = 0; k < CH; ++k)
+                            y[k] = (sees >> (k0 + k)) & 1u ? y[k] : -INFINITY;
+                    }
+                    __syncwarp();
+                };
+                auto exponents = [&](int k0) {
                     tc_ld(y, src + k0);
                     tc_wait_ld(y);
 #pragma unroll
                     for (int k = 0; k < CH; k += 2)
                         mul_pair(y + k, sl2);
-                    apply_mask(k0);
+                    if constexpr (C::REG_REF) {
 #pragma unroll
-                    for (int k = 0; k < CH; ++k) {
-                        const float x = redux_max(y[k]);
-                        mine = lane == k0 + k ? x : mine;
+                        for (int k = 0; k < CH; k += 2)
+                            sub_pair(y + k, ref + k0 + k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < CH; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(&s_ref[wg][k0 + k]);
+                            sub_pair(y + k, &f.x);
+                            sub_pair(y + k + 2, &f.z);
+                        }
+                    }
+                    apply_mask(k0);
+                };
+                // the second time round, after the references moved, no weight passes the limit
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int k0 = 0; k0 < NC; k0 += CH) {
+                        exponents(k0);
+#pragma unroll
+                        for (int k = 0; k < CH; ++k)
+                            top = fmaxf(top, y[k]);
+                    }
+                    if (__builtin_expect(pass == 1 || !group_any(3 + wg, top > kAttLimit), 1))
+                        break;
+                    float mine = -INFINITY;  // the warp's largest logit of row `lane`
+#pragma unroll
+                    for (int k0 = 0; k0 < NC; k0 += CH) {
+                        tc_ld(y, src + k0);
+                        tc_wait_ld(y);
+#pragma unroll
+                        for (int k = 0; k < CH; k += 2)
+                            mul_pair(y + k, sl2);
+                        apply_mask(k0);
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) {
+                            const float x = redux_max(y[k]);
+                            mine = lane == k0 + k ? x : mine;
+                        }
+                    }
+                    const float old = my_ref();
+                    if (lane < NC)
+                        s_red[wg][lane][qd] = mine;
+                    named_bar(3 + wg, 128);
+                    const float4 r = *reinterpret_cast<const float4*>(s_red[wg][lane < NC ? lane : 0]);
+                    const float m = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
+                    // a maximum beyond 2^20 is its own reference: 13 would be lost in it
+                    const float next = fmaxf(old, fabsf(m) < 1048576.0f ? m - kAttShift : m);
+                    const float alpha = next == old ? 1.0f : ex2_ftz(old - next);
+                    if constexpr (!C::REG_REF) {
+                        if (qd == 0)
+                            s_ref[wg][lane % NC] = next;  // every warp has read the old one
+                        named_bar(3 + wg, 128);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) {
+                        if constexpr (C::REG_REF)
+                            ref[k] = __shfl_sync(0xffffffffu, next, k);
+                        const float f = __shfl_sync(0xffffffffu, alpha, k);
+                        l[k] *= f;
+#pragma unroll
+                        for (int h = 0; h < MH; ++h)
+                            o[h][k] *= f;
                     }
                 }
-                const float old = my_ref();
-                if (lane < NC)
-                    s_red[wg][lane][qd] = mine;
-                named_bar(3 + wg, 128);
-                const float4 r = *reinterpret_cast<const float4*>(s_red[wg][lane < NC ? lane : 0]);
-                const float m = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
-                // a maximum beyond 2^20 is its own reference: 13 would be lost in it
-                const float next = fmaxf(old, fabsf(m) < 1048576.0f ? m - kAttShift : m);
-                const float alpha = next == old ? 1.0f : ex2_ftz(old - next);
-                if constexpr (!C::REG_REF) {
-                    if (qd == 0)
-                        s_ref[wg][lane % NC] = next;  // every warp has read the old one
-                    named_bar(3 + wg, 128);
-                }
+                uint8_t* prow = sm + C::O_P + (32 * qd + lane) * 128;
+                const int sw = lane & 7;  // token position % 8
 #pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    if constexpr (C::REG_REF)
-                        ref[k] = __shfl_sync(0xffffffffu, next, k);
-                    const float f = __shfl_sync(0xffffffffu, alpha, k);
-                    l[k] *= f;
+                for (int k0 = 0; k0 < NC; k0 += CH) {
+                    if (NC > CH)
+                        exponents(k0);
+                    uint32_t hi[CH / 2], lo[CH / 2];
 #pragma unroll
-                    for (int h = 0; h < MH; ++h)
-                        o[h][k] *= f;
-                }
-            }
-            uint8_t* prow = sm + C::O_P + (32 * qd + lane) * 128;
-            const int sw = lane & 7;  // token position % 8
-#pragma unroll
-            for (int k0 = 0; k0 < NC; k0 += CH) {
-                if (NC > CH)
-                    exponents(k0);
-                uint32_t hi[CH / 2], lo[CH / 2];
-#pragma unroll
-                for (int k = 0; k < CH; k += 2) {
-                    y[k] = ex2_ftz(y[k]);
-                    y[k + 1] = ex2_ftz(y[k + 1]);
-                    add_pair(l + k0 + k, y + k);
-                    split_pair(y + k, hi[k / 2], lo[k / 2]);
-                }
-                const int r0 = wg * NC + k0;
-                if constexpr (NC < 8) {  // half a 16-byte chunk of each term
-                    const int at = (r0 & 4) << 1;
-                    *reinterpret_cast<uint2*>(prow + (((r0 >> 3) ^ sw) << 4) + at) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(prow + (((NR / 8 + (r0 >> 3)) ^ sw) << 4) + at) = make_uint2(lo[0], lo[1]);
-                } else {
+                    for (int k = 0; k < CH; k += 2) {
+                        y[k] = ex2_ftz(y[k]);
+                        y[k + 1] = ex2_ftz(y[k + 1]);
+                        add_pair(l + k0 + k, y + k);
+                        split_pair(y + k, hi[k / 2], lo[k / 2]);
+                    }
+                    const int r0 = wg * NC + k0;
 #pragma unroll
                     for (int k = 0; k < CH; k += 8) {  // eight rows: a 16-byte chunk of each term
                         const int ck = (r0 + k) >> 3;
@@ -1066,8 +1062,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                             *reinterpret_cast<uint4*>(row + C::PTERM + (((ck & 7) ^ sw) << 4)) = vl;
                     }
                 }
-            }
-            publish();  // O(i) is issued
+                publish();  // O(i) is issued
             }
             if (i + 2 < n) {
                 if (i >= -1)
@@ -1076,35 +1071,34 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 publish();  // S(i + 2) is issued
             }
             if (i >= 0) {
-            wait(&s_odone, i);
-            tc_fence_after();
-            constexpr int OC = NC < 8 ? NC : 8;
+                wait(&s_odone, i);
+                tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < MH; ++h)
+                for (int h = 0; h < MH; ++h)
 #pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += OC) {
-                    float y[OC];
-                    const uint32_t src = tm + C::TM_O + h * C::PN + wg * NC + k0 + lanes;
-                    tc_ld(y, src);
-                    if constexpr (C::STACK) {
-                        float z[OC];
-                        tc_ld(z, src + NR);
-                        tc_wait_ld(y);
-                        tc_wait_ld(z);
+                    for (int k0 = 0; k0 < NC; k0 += 8) {
+                        float y[8];
+                        const uint32_t src = tm + C::TM_O + h * C::PN + wg * NC + k0 + lanes;
+                        tc_ld(y, src);
+                        if constexpr (C::STACK) {
+                            float z[8];
+                            tc_ld(z, src + NR);
+                            tc_wait_ld(y);
+                            tc_wait_ld(z);
 #pragma unroll
-                        for (int k = 0; k < OC; k += 2)
-                            add_pair(y + k, z + k);
-                    } else {
-                        tc_wait_ld(y);
+                            for (int k = 0; k < 8; k += 2)
+                                add_pair(y + k, z + k);
+                        } else {
+                            tc_wait_ld(y);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2)
+                            add_pair(o[h] + k0 + k, y + k);
                     }
-#pragma unroll
-                    for (int k = 0; k < OC; k += 2)
-                        add_pair(o[h] + k0 + k, y + k);
+                if (__builtin_expect(d.last, 0)) {
+                    finish(i);
+                    named_bar(2, C::WORKERS);  // P's buffer, where the sums went, may be written
                 }
-            if (__builtin_expect(d.last, 0)) {
-                finish(i);
-                named_bar(2, C::WORKERS);  // P's buffer, where the sums went, may be written
-            }
             }
             if (i >= -1 && i + 1 < n)
                 values(i + 1);
@@ -1163,22 +1157,10 @@ cudaError_t attend_launch_rows(const kivi_cache& c, const AttendArgs& a, float* 
 {
     using C = AttCfg<D, NR>;
     auto kern = attend_kernel<D, NR, B>;
-    AttPlan pl;
-    pl.lgG = c.G == 32 ? 5 : c.G == 64 ? 6 : 7;
-    pl.M = a.Hq / c.H * a.N;
-    pl.RT = (pl.M + NR - 1) / NR;
-    pl.kub = 4 * D * c.bits_k;
-    pl.vub = 4 * D * c.bits_v;
-    for (pl.su = 4;; pl.su = 2) {  // a tile per stage where one fits, else half a tile
-        pl.kst = pl.su * (pl.kub + 8 * D);
-        pl.vst = pl.su * (pl.vub + 256 * (D / c.G));
-        pl.ns = cmin(C::RING / (pl.kst + pl.vst), kAttMaxStages);
-        if (pl.ns > 0 || pl.su == 2)
-            break;
-    }
+    const AttPlan pl = att_plan<D, NR>(c.G, c.bits_k, c.bits_v, a.Hq / c.H * a.N);
     if (pl.ns < 1)
         return cudaErrorInvalidConfiguration;
-    const int smem = 1024 + C::O_RING + pl.ns * (pl.kst + pl.vst);
+    const int smem = att_smem_bytes<D, NR>(pl);
     static int allowed[64];
     cudaError_t e = allow_smem(kern, kAttSmem - C::STATIC, allowed);
     if (e != cudaSuccess)

@@ -7,14 +7,20 @@
 namespace kivi {
 
 // Up to 16 query rows of a KV head (8 at D = 256) go to the warp kernel, more
-// to the tcgen05 kernel, whose products cost the same up to 32 rows.
+// to the tcgen05 kernel, whose products cost the same up to 32 rows.  Both
+// sides, when the tcgen05 kernel had a 16-row tile: 1 row of 64 ragged
+// sequences 168 against 303 us, 8 rows of an int4 prefix 170 against 263, 16
+// rows of eight sequences 126 against 128.  Beyond, the warp kernel would need
+// the registers of 24 rows' O.
 template <int D, int B>
 cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
 {
     KIVI_SET_CHECK_RANGES(c, s, {{a.q, (size_t)c.B * a.Hq * a.N * D * 2}, {a.out, (size_t)c.B * a.Hq * a.N * D * 4},
-                                 {a.k, (size_t)c.B * c.H * a.N * D * 2}, {a.v, (size_t)c.B * c.H * a.N * D * 2},
+                                 {a.k ? a.k : (const void*)a.blocks,  // a call has drafts or a list of groups
+                                  (size_t)c.B * c.H * (a.k ? (size_t)a.N * D * 2 : (size_t)a.n_keep * 4)},
+                                 {a.v, (size_t)c.B * c.H * a.N * D * 2},
                                  {a.mask, (size_t)c.B * a.N * ((a.N + 63) / 64) * 8}, {a.n_draft, (size_t)c.B * 4},
-                                 {a.blocks, (size_t)c.B * c.H * a.n_keep * 4}});
+                                 {ws, attend_ws_bytes(c, a.Hq, a.N)}});
     const int M = a.Hq / c.H * a.N;
     if (attend_by_warp(D, M)) {
         if constexpr (D != 256)

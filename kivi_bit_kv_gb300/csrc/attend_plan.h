@@ -1,5 +1,5 @@
-// attend_plan.h -- shapes of the sparse and tree attention kernel (attend.cuh):
-// its roles, shared memory, TMEM and workspace.
+// attend_plan.h -- shapes of the sparse and tree attention kernels (attend.cuh,
+// attend_warp.cuh): shared memory, TMEM and workspace.
 #pragma once
 
 #include <stddef.h>
@@ -15,10 +15,10 @@ namespace kivi {
 
 constexpr int kAttSmem = 227 * 1024;          // shared memory of one CTA alone on its SM
 constexpr int kAttTile = 128;                 // tokens per tile
-constexpr int kAttMaxCTAs = 320;              // workspace bound on the grid
+constexpr int kAttMaxCTAs = 320;              // bound on the grid, which sizes the workspace
 constexpr int kAttMaxStages = 8;              // of each ring
 constexpr int kAttDescs = 16;                 // tile descriptors kept in shared memory
-constexpr int kAttCutInts = 8;
+constexpr int kAttCutInts = 4;                 // of a cut row tile: set, sequence, head or row tile, last range
 constexpr int kAttHeaderFloats = 4;
 constexpr float kAttShift = 13.0f;            // a row's largest weight is 2^13 when its reference is set ...
 constexpr float kAttLimit = 15.9f;            // ... and stays below 2^15.9, inside fp16
@@ -95,5 +95,65 @@ struct AttPlan {
     int kst, vst;         // bytes of a stage: keys, values
     int kub, vub;         // code bytes of 32 tokens: keys, values
 };
+
+template <int D, int NR>
+AttPlan att_plan(int G, int bits_k, int bits_v, int M)
+{
+    using C = AttCfg<D, NR>;
+    AttPlan pl;
+    pl.lgG = G == 32 ? 5 : G == 64 ? 6 : 7;
+    pl.M = M;
+    pl.RT = (M + NR - 1) / NR;
+    pl.kub = 4 * D * bits_k;
+    pl.vub = 4 * D * bits_v;
+    for (pl.su = 4;; pl.su = 2) {  // a tile per stage where one fits, else half a tile
+        pl.kst = pl.su * (pl.kub + 8 * D);
+        pl.vst = pl.su * (pl.vub + 256 * (D / G));
+        pl.ns = C::RING / (pl.kst + pl.vst);
+        pl.ns = pl.ns < kAttMaxStages ? pl.ns : kAttMaxStages;
+        if (pl.ns > 0 || pl.su == 2)
+            return pl;
+    }
+}
+
+template <int D, int NR>
+int att_smem_bytes(const AttPlan& pl)
+{
+    return 1024 + AttCfg<D, NR>::O_RING + pl.ns * (pl.kst + pl.vst);
+}
+
+// The warp kernel (attend_warp.cuh).
+constexpr int kWarpStatic = 4 * 1024;                      // bound on its static shared arrays
+
+template <int D, int NT>
+struct WarpCfg {
+    static constexpr int NR = 8 * NT;                      // rows
+    static constexpr int WARPS = NT == 2 ? 12 : D == 256 ? 10 : 16;  // by registers: 168, 200, 128 a thread
+    static constexpr int HAT = 64 * D;                     // K_hat or V_hat of a unit
+    static_assert(D != 256 || NT == 1, "registers");
+};
+
+struct WarpPlan {
+    int lgG, M, warps;    // log2 G, query rows of a KV head, warps per CTA
+    int kub, vub;         // code bytes of 32 tokens
+    int kst, vst;         // with statistics
+    int bytes;            // shared memory of a warp
+};
+
+template <int D, int NT>
+WarpPlan warp_plan(int G, int bits_k, int bits_v, int M)
+{
+    WarpPlan pl;
+    pl.lgG = G == 32 ? 5 : G == 64 ? 6 : 7;
+    pl.M = M;
+    pl.kub = 4 * D * bits_k;
+    pl.vub = 4 * D * bits_v;
+    pl.kst = pl.kub + 8 * D;
+    pl.vst = pl.vub + 256 * (D / G);
+    pl.bytes = WarpCfg<D, NT>::HAT + pl.kst + pl.vst;
+    const int fit = (kAttSmem - kWarpStatic) / pl.bytes;
+    pl.warps = fit < WarpCfg<D, NT>::WARPS ? fit : WarpCfg<D, NT>::WARPS;
+    return pl;
+}
 
 }  // namespace kivi

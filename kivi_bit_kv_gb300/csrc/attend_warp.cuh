@@ -31,26 +31,19 @@
 // Every wait on an mbarrier gives up after some two seconds: it records
 // KIVI_ETIMEOUT in the workspace's status word; the warp then leaves once its
 // copies have landed (a bounded wait as well).
+//
+// Measured: one row a KV head over 1024 listed tokens and the residual of 64
+// ragged int2 sequences of 32 heads (418 MB): 158 us, 2.6 TB/s; 8 rows over a
+// 2065-token int4 prefix of 32 x 32 heads (420 MB): 166 us, 2.5 TB/s; 16 rows
+// over eight int2 sequences of 4096 tokens (152 MB): 124 us.  The issue rate
+// bounds it: some 1200 instructions a unit of 4096 elements of K and of V each,
+// at half an instruction a cycle from the four warps that a scheduler's
+// registers hold; deeper unrolling made it slower (instruction fetch).
 #pragma once
 
 #include "attend.cuh"
 
 namespace kivi {
-
-template <int D, int NT>
-struct WarpCfg {
-    static constexpr int NR = 8 * NT;                      // rows
-    static constexpr int WARPS = NT == 2 ? 12 : D == 256 ? 10 : 16;  // by registers: 168, 200, 128 a thread
-    static constexpr int HAT = 64 * D;                     // K_hat or V_hat of a unit
-    static_assert(D != 256 || NT == 1, "registers");
-};
-
-struct WarpPlan {
-    int lgG, M, warps;    // log2 G, query rows of a KV head, warps per CTA
-    int kub, vub;         // code bytes of 32 tokens
-    int kst, vst;         // with statistics
-    int bytes;            // shared memory of a warp
-};
 
 // A sequence's counts, in units: quantized units, then fp16 ones.
 struct WarpSeq {
@@ -808,21 +801,12 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
 {
     using C = WarpCfg<D, NT>;
     auto kern = attend_warp_kernel<D, NT, B>;
-    WarpPlan pl;
-    pl.lgG = c.G == 32 ? 5 : c.G == 64 ? 6 : 7;
-    pl.M = a.Hq / c.H * a.N;
-    pl.kub = 4 * D * c.bits_k;
-    pl.vub = 4 * D * c.bits_v;
-    pl.kst = pl.kub + 8 * D;
-    pl.vst = pl.vub + 256 * (D / c.G);
-    pl.bytes = C::HAT + pl.kst + pl.vst;
-    constexpr int kStatic = 4 * 1024;  // bound on the kernel's static shared arrays
-    pl.warps = cmin((kAttSmem - kStatic) / pl.bytes, C::WARPS);
+    const WarpPlan pl = warp_plan<D, NT>(c.G, c.bits_k, c.bits_v, a.Hq / c.H * a.N);
     if (pl.warps < 1)
         return cudaErrorInvalidConfiguration;
     const int smem = pl.warps * pl.bytes;
     static int allowed[64];
-    cudaError_t e = allow_smem(kern, kAttSmem - kStatic, allowed);
+    cudaError_t e = allow_smem(kern, kAttSmem - kWarpStatic, allowed);
     if (e != cudaSuccess)
         return e;
     const int N = cmin(sm_count(), kAttMaxCTAs / 2);

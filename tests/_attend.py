@@ -53,7 +53,9 @@ def attend_ref(q, K, V, sm):
     acts on the sum of weights and on the weighted sum.  The weighted sum adds
     256 products per 128 tokens and one term per 128 tokens, the sum of the
     weights n/128 + 64 terms, each addition at most 2^-23 of the partial sum
-    of magnitudes."""
+    of magnitudes.  (Up to 16 rows: 64 products and one rounded addition, 2^-24,
+    per 32 tokens; a sum of weights adds four per 32 tokens of one warp's range,
+    32 of which are 128 additions of 2^-24.)"""
     n = K.shape[0]
     if n == 0:
         z = torch.zeros_like(q)
