@@ -249,7 +249,7 @@ __device__ __forceinline__ AttSeq att_seq(const kivi_cache& c, const AttendArgs&
 {
     AttSeq s;
     s.len = min(max(ldg_checked(c.len + b), 0), c.Tmax);
-    s.Tq = quantized_tokens(s.len, c.G, c.R);
+    s.Tq = max(s.len - c.R, 0) >> lgG << lgG;
     s.nq = a.blocks ? min(a.n_keep, s.Tq >> lgG) << lgG : s.Tq;
     s.nd = 0;
     if (a.k)

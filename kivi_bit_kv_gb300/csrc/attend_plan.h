@@ -138,6 +138,7 @@ struct WarpPlan {
     int kub, vub;         // code bytes of 32 tokens
     int kst, vst;         // with statistics
     int bytes;            // shared memory of a warp
+    int by_row;           // records of cut rows by row, not by range
 };
 
 template <int D, int NT>
@@ -153,6 +154,7 @@ WarpPlan warp_plan(int G, int bits_k, int bits_v, int M)
     pl.bytes = WarpCfg<D, NT>::HAT + pl.kst + pl.vst;
     const int fit = (kAttSmem - kWarpStatic) / pl.bytes;
     pl.warps = fit < WarpCfg<D, NT>::WARPS ? fit : WarpCfg<D, NT>::WARPS;
+    pl.by_row = 0;
     return pl;
 }
 

@@ -81,59 +81,77 @@ __device__ __forceinline__ void warp_next(WarpWalk& w, const kivi_cache& c, cons
     }
 }
 
-// Range `index` of range[3] ranges (at most count, of two units or more): units [range[0],
-// range[1]) of range[2], none beyond the last range, and the
-// position of its first unit.  One warp.
-static __device__ __noinline__ void warp_locate(const kivi_cache* c, const AttendArgs* a, int lgG, long long index,
-                                                long long count, long long* range, WarpWalk* first)
+// The split of all units into ranges of `base` units, the first `rem` of them
+// one longer, and where this warp's lies.  32 bits hold every unit number: the
+// codes of a unit take 1 KB of device memory at least, a row's ring more.
+struct WarpRange {
+    int first, n, base, rem;
+    // the range that unit u lies in
+    __device__ __forceinline__ int of(int u) const
+    {
+        const int longer = rem * (base + 1);
+        return u < longer ? u / (base + 1) : rem + (u - longer) / base;
+    }
+};
+
+// Range `index` of up to `count` (empty beyond the last) and the position of its
+// first unit.  One warp.
+static __device__ __noinline__ void warp_locate(const kivi_cache* c, const AttendArgs* a, int lgG, int index, int count,
+                                                WarpRange* range, WarpWalk* first)
 {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
+    int total = 0;
+    WarpWalk w;
+    w.b = lane;
+    w.s.nt = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < c->B; b0 += 32) {
-        long long n = b0 + lane < c->B ? (long long)warp_seq(*c, *a, lgG, b0 + lane).nt * c->H : 0;
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1)
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        total += n;
+    for (int b = lane; b - lane < c->B; b += 32) {
+        if (b < c->B)
+            w.s = warp_seq(*c, *a, lgG, b);
+        total += __reduce_add_sync(0xffffffffu, b < c->B ? w.s.nt * c->H : 0);
     }
-    count = min(count, (total + 1) / 2);  // two units a range at least: fewer pieces to merge
-    const long long p = index < count ? total * index / count : total;
-    if (lane == 0) {
-        range[0] = p;
-        range[1] = index < count ? total * (index + 1) / count : total;
-        range[2] = total;
-        range[3] = count;
+    // A unit a range or more, and 32 ranges a row: past that merging the pieces
+    // costs more than the warps save (four sequences of 8 heads and 69 units:
+    // 17.7 us with a unit each, 16.6 with two or three).
+    count = min(count, total);
+    if (c->B * c->H < count / 32)
+        count = 32 * c->B * c->H;
+    WarpRange r = {0, 0, 1, 0};
+    if (index < count) {
+        r.base = (int)((unsigned)total / (unsigned)count);
+        r.rem = total - r.base * count;
+        r.first = index * r.base + min(index, r.rem);
+        r.n = r.base + (index < r.rem);
     }
+    if (lane == 0)
+        *range = r;
     __syncwarp();
-    if (p == total)
+    if (r.n == 0)
         return;
-    long long before = 0;
+    int before = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < c->B; b0 += 32) {
-        WarpWalk w;
-        w.b = b0 + lane;
-        w.s.nt = 0;
-        if (w.b < c->B)
+    for (;;) {
+        if (c->B > 32 && w.b < c->B)  // else as in the first pass
             w.s = warp_seq(*c, *a, lgG, w.b);
-        const long long n = (long long)w.s.nt * c->H;
-        long long inc = n;
-#pragma unroll 1
+        const int n = w.b < c->B ? w.s.nt * c->H : 0;
+        int inc = n;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            const int t = __shfl_up_sync(0xffffffffu, inc, o);
             inc += lane >= o ? t : 0;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, p < before + inc);
-        if (hit) {
+        const unsigned hit = __ballot_sync(0xffffffffu, r.first < before + inc);
+        if (hit) {  // in the end: first < total
             if (lane == __ffs(hit) - 1) {
-                const long long at = p - (before + inc - n);
-                w.h = (int)(at / w.s.nt);
-                w.j = (int)(at % w.s.nt);
+                const unsigned at = r.first - (before + inc - n);
+                w.h = (int)(at / (unsigned)w.s.nt);
+                w.j = (int)(at - (unsigned)w.h * w.s.nt);
                 *first = w;
             }
             break;
         }
         before = __shfl_sync(0xffffffffu, before + inc, 31);
+        w.b += 32;
     }
     __syncwarp();
 }
@@ -274,11 +292,13 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
     extern __shared__ __align__(128) uint8_t att_smem[];
     __shared__ uint64_t s_full[C::WARPS][2];
     __shared__ WarpWalk s_walk[C::WARPS];
-    __shared__ long long s_range[C::WARPS][4];
+    __shared__ WarpRange s_range[C::WARPS];
     __shared__ int s_abort[C::WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int g = lane >> 2, tq = lane & 3;
-    const long long index = (long long)blockIdx.x * pl.warps + warp, count = (long long)gridDim.x * pl.warps;
+    // neighbouring ranges on different SMs: few ranges, or the longer ones, are
+    // spread over all of them
+    const int index = warp * gridDim.x + blockIdx.x, count = gridDim.x * pl.warps;
     int* status = reinterpret_cast<int*>(ws);
     if (lane == 0) {
         mbar_init(&s_full[warp][0], 1);
@@ -288,11 +308,11 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
             *status = KIVI_OK;
         mbar_fence_init();
     }
-    warp_locate(&c, &a, pl.lgG, index, count, s_range[warp], &s_walk[warp]);
-    const int n = (int)(s_range[warp][1] - s_range[warp][0]);
-    int* cut = reinterpret_cast<int*>(ws + kAttHeaderFloats) + (size_t)index * kAttCutInts;
-    if (lane == 0)
-        cut[0] = 0;
+    warp_locate(&c, &a, pl.lgG, index, count, &s_range[warp], &s_walk[warp]);
+    const int n = s_range[warp].n;
+    int4* cuts = reinterpret_cast<int4*>(ws + kAttHeaderFloats);
+    if (!pl.by_row && lane == 0)
+        cuts[index] = make_int4(-1, 0, 0, 0);
     asm volatile("griddepcontrol.launch_dependents;");
     if (n == 0)
         return;
@@ -640,6 +660,8 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 #pragma unroll
                 for (int k = 0; k < NCOL; ++k)
                     scale[k] = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
+                if (pl.by_row && lane == 0)
+                    cuts[w.b * c.H + w.h] = make_int4(-1, 0, 0, 0);
             } else {
                 dst = warp_part(ws, D, pl.M, index, mid ? 0 : 1);
                 if (g == 0) {
@@ -653,13 +675,10 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                     }
                 }
                 if (!tail && !mid && lane == 0) {
-                    // the row starts in this range and its last unit, end - 1, is in range `last`:
-                    // the first with total (last + 1) / count >= end
-                    const long long end = s_range[warp][1] + (w.s.nt - 1 - w.j);
-                    cut[1] = w.b;
-                    cut[2] = w.h;
-                    cut[3] = (int)((end * s_range[warp][3] + s_range[warp][2] - 1) / s_range[warp][2] - 1);
-                    cut[0] = 1;
+                    // the row starts in this range; where its last unit lies
+                    const WarpRange& r = s_range[warp];
+                    cuts[pl.by_row ? w.b * c.H + w.h : index] =
+                        make_int4(r.of(r.first + n - 1 + (w.s.nt - 1 - w.j)), index, w.b, w.h);
                 }
             }
 #pragma unroll
@@ -687,27 +706,30 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
     }
 }
 
-// Merges the pieces of the rows that ranges cut: block i takes the row that
-// starts in range i and ends in a later one, piece by piece in order.
-static __global__ void __launch_bounds__(kAttCombineThreads)
+// Merges the pieces of the rows that ranges cut, piece by piece in order: block
+// i takes row i (few rows, 512 threads: each has many pieces), or the row that
+// starts in range i and ends in a later one (256 threads).
+template <int T>
+__global__ void __launch_bounds__(T)
 attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ AttendArgs a, int M,
-                           float* __restrict__ ws)
+                           int ranges, float* __restrict__ ws)
 {
-    const int D = c.D, i = blockIdx.x;
+    const int D = c.D;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int* cut = reinterpret_cast<const int*>(ws + kAttHeaderFloats) + (size_t)i * kAttCutInts;
-    if (cut[0] == 0)
+    const int4 cut = reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[blockIdx.x];
+    // a sequence without drafts, or a kernel that gave up, leaves its records as they were
+    const int last = cut.x, i = cut.y, b = cut.z, h = cut.w;
+    if (i < 0 || last <= i || last >= ranges || b < 0 || b >= c.B || h < 0 || h >= c.H)
         return;
-    const int b = cut[1], h = cut[2], last = cut[3];
     const int nd = a.k ? (a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), a.N) : a.N) : 1;
     // 64 pieces at a time: their weights (a warp per row, a lane per two pieces),
     // then the weighted sum of their outputs, four channels a thread and the
     // pieces spread over the threads that are left
     constexpr int P = 64;
     __shared__ float s_w[16][P], s_m[16], s_l[16], s_f[16];
-    __shared__ float4 s_o[kAttCombineThreads];
+    __shared__ float4 s_o[T];
     const int t = threadIdx.x, lane = t & 31, n4 = M * D / 4;
-    const int groups = n4 < kAttCombineThreads ? kAttCombineThreads / n4 : 1;
+    const int groups = n4 < T ? T / n4 : 1;
     if (t < M) {
         s_m[t] = -INFINITY;
         s_l[t] = 0.0f;
@@ -721,7 +743,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
         const int np = min(P, last + 1 - k0);
         __syncthreads();
 #pragma unroll 1
-        for (int r = t >> 5; r < M; r += kAttCombineThreads / 32) {
+        for (int r = t >> 5; r < M; r += T / 32) {
             float m[2], l[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -752,13 +774,13 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int e4 = (t + k * kAttCombineThreads) % (groups * n4) % n4, grp = groups > 1 ? t / n4 : 0;
-            if (grp >= groups || (k > 0 && t + k * kAttCombineThreads >= n4))
+            const int e4 = (t + k * T) % (groups * n4) % n4, grp = groups > 1 ? t / n4 : 0;
+            if (grp >= groups || (k > 0 && t + k * T >= n4))
                 continue;
             const int r = e4 * 4 / D;
             const float f = s_f[r];
             float4 x = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
-#pragma unroll 4
+#pragma unroll 8
             for (int q = grp; q < np; q += groups) {
                 const float4 v = *reinterpret_cast<const float4*>(warp_part(ws, D, M, k0 + q, k0 + q == i) + 4 * e4);
                 const float wq = s_w[r][q];
@@ -784,7 +806,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int e4 = t + k * kAttCombineThreads, r = e4 * 4 / D;
+        const int e4 = t + k * T, r = e4 * 4 / D;
         if (e4 < n4 && r % a.N < nd) {
             const float inv = s_l[r] > 0.0f ? 1.0f / s_l[r] : 0.0f;
             st_checked(reinterpret_cast<float4*>(
@@ -801,7 +823,7 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
 {
     using C = WarpCfg<D, NT>;
     auto kern = attend_warp_kernel<D, NT, B>;
-    const WarpPlan pl = warp_plan<D, NT>(c.G, c.bits_k, c.bits_v, a.Hq / c.H * a.N);
+    WarpPlan pl = warp_plan<D, NT>(c.G, c.bits_k, c.bits_v, a.Hq / c.H * a.N);
     if (pl.warps < 1)
         return cudaErrorInvalidConfiguration;
     const int smem = pl.warps * pl.bytes;
@@ -810,21 +832,23 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
     if (e != cudaSuccess)
         return e;
     const int N = cmin(sm_count(), kAttMaxCTAs / 2);
+    pl.by_row = (long long)c.B * c.H <= 2 * N;  // few rows: a block per row merges them, else one per range
     kern<<<N, 32 * pl.warps, smem, s>>>(c, a, pl, ws);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     // the combine's CTAs are scheduled while the attention drains
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(N * pl.warps);
-    cfg.blockDim = dim3(kAttCombineThreads);
+    cfg.gridDim = dim3(pl.by_row ? c.B * c.H : N * pl.warps);
+    cfg.blockDim = dim3(pl.by_row ? 512 : 256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_warp_combine_kernel, c, a, pl.M, ws);
+    return cudaLaunchKernelEx(&cfg, pl.by_row ? attend_warp_combine_kernel<512> : attend_warp_combine_kernel<256>, c, a,
+                              pl.M, N * pl.warps, ws);
 }
 
 }  // namespace kivi
