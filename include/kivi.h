@@ -358,8 +358,9 @@ int32_t kivi_sparse_attention(const kivi_cache* c, const uint16_t* q,
  * [B][Hq][N][D]; 1 <= N <= KIVI_MAX_DRAFT.  n_draft (device int32 [B], or NULL
  * for N everywhere) gives the drafted tokens of each sequence, taken as
  * min(n_draft[b], N) (0 if negative): k, v and mask bits of tokens from there
- * on are not read, and their rows of out are left as they were.  A row that
- * attends nothing gets out = 0.  ws: as for kivi_sparse_attention, >=
+ * on are not read, and their rows of out are left as they were.  A drafted
+ * token's k and v reach only the rows that attend it, NaN and infinities
+ * included.  A row that attends nothing gets out = 0.  ws: as for kivi_sparse_attention, >=
  * kivi_attend_workspace_bytes(c, Hq, N) bytes; status word, sharing and
  * determinism as there.
  */

@@ -208,6 +208,30 @@ __device__ __forceinline__ void split_pair(float* p, uint32_t& hi, uint32_t& lo)
     sub_pair(p, h);
     lo = h2_bits(__floats2half2_rn(p[0], p[1]));
 }
+// A value that is not finite must not reach the product: its weight of 0 in a
+// row that does not attend its token would still make the row NaN.  The fp16
+// values of drafted tokens are cleared of such halves here (true if there were
+// any), and added to the stored rows that attend them (a row may get one twice,
+// where two pieces of it hold drafts: the sum is the same).
+__device__ __forceinline__ bool clear_nonfinite(uint32_t (&q)[8])
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        any |= (q[k] & 0x7C007C00u) + 0x04000400u;  // bits 15, 31: an exponent of all ones
+    if (!(any & 0x80008000u))
+        return false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        q[k] &= ~(((((q[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) >> 15) * 0xFFFFu);
+    return true;
+}
+// An fp16 value if it is not finite, else 0.
+__device__ __forceinline__ float nonfinite(const uint16_t* p)
+{
+    const float x = __half2float(__ushort_as_half(ldg_checked(p)));
+    return isfinite(x) ? 0.0f : x;
+}
 // Waits for the phase of parity `parity` of mbarrier b; false, with the abort
 // flag set and the timeout recorded in *status (unless null), if it has not
 // completed within kAttWaitTries attempts (some four microseconds each) or *abort
@@ -523,8 +547,8 @@ static __device__ __noinline__ void att_seen(const AttendArgs* a, const AttDesc*
 // of a token: an element of each channel's row of K, run order in V.
 template <int D, int GROUPS>
 static __device__ __noinline__ void att_fp16_rows(const kivi_cache* c, const AttendArgs* a, const AttPlan* pl,
-                                                  const AttDesc* d, const unsigned long long* seen, uint8_t* dst,
-                                                  int which, int t)
+                                                  const AttDesc* d, const unsigned long long* seen, int* dirty,
+                                                  uint8_t* dst, int which, int t)
 {
     const int e = which == 0 ? t & 127 : t / GROUPS, part = which == 0 ? t >> 7 : t % GROUPS;
     if (e < 32 * d->nuq)
@@ -554,7 +578,9 @@ static __device__ __noinline__ void att_fp16_rows(const kivi_cache* c, const Att
             for (int k = 0; k < 16; ++k)
                 *reinterpret_cast<uint16_t*>(kd + (c0 + k) * 128 + (kx ^ ((k & 7) << 4))) = u4_half(k < 8 ? y : z, k & 7);
         } else {
-            const uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+            uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+            if (j >= 0 && clear_nonfinite(q))
+                *dirty = 1;
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -566,6 +592,30 @@ static __device__ __noinline__ void att_fp16_rows(const kivi_cache* c, const Att
             const int cc = (c0 & 63) * 2;
             *reinterpret_cast<uint4*>(run + (cc ^ vx)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(run + ((cc + 16) ^ vx)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// Adds to a thread's stored channels ch, ch + 128 of the rows r0 + k (bit k of
+// `rows`) the values that are not finite of the drafts which those rows attend.
+template <int D, int MH>
+static __device__ __noinline__ void att_add_nonfinite(const AttendArgs* a, const AttDesc* d, const uint16_t* v, int r0,
+                                                      uint32_t rows, int ch, float* dst)
+{
+    const int W = (a->N + 63) >> 6;
+    if (ch >= D)
+        return;
+#pragma unroll 1
+    for (int x = 0; x < d->nd * MH; ++x) {
+        const int j = x / MH, half = 128 * (x % MH);
+        const float y = nonfinite(v + (size_t)j * D + ch + half);
+        if (y == 0.0f)
+            continue;
+#pragma unroll 1
+        for (uint32_t left = rows; left; left &= left - 1) {
+            const int k = __ffs(left) - 1, i = (r0 + k) % a->N;
+            if (i < d->nd && (ldg_checked(a->mask + ((size_t)d->b * a->N + i) * W + (j >> 6)) >> (j & 63)) & 1)
+                st_checked(dst + k * D + half, dst[k * D + half] + y);
         }
     }
 }
@@ -583,6 +633,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
     extern __shared__ uint8_t att_smem[];
     __shared__ AttDesc s_desc[kAttDescs];
     __shared__ unsigned long long s_seen[4][4];                // drafts any row attends, by tile
+    __shared__ int s_dirty;                                    // values of some draft were cleared
     __shared__ __align__(16) float s_red[C::GROUPS][NC][4];            // maxima: [row group][row][lane quadrant]
     __shared__ float s_part[C::GROUPS][128];
     __shared__ __align__(16) float s_ref[C::GROUPS][C::REG_REF ? 1 : NC];
@@ -603,7 +654,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
     } else if (warp == kMmaWarp) {
         tc_alloc(&s_tmem, C::TM_COLS);
         if (lane == 0) {
-            s_abort = s_never = 0;
+            s_abort = s_never = s_dirty = 0;
             if (cta == 0)
                 *status = KIVI_OK;
             for (int i = 0; i < pl.ns; ++i) {
@@ -810,7 +861,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
             if (__builtin_expect(d.nuq < 4, 0)) {
                 if (d.nd > 0 && d.f0 + kAttTile > d.res)
                     att_seen<C::WORKERS>(&a, &d, s_seen[i & 3], t);
-                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], sm + C::O_K, 0, t);
+                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], &s_dirty, sm + C::O_K, 0, t);
             }
         };
         auto values = [&](int i) {
@@ -830,7 +881,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 release(1);
             }
             if (__builtin_expect(d.nuq < 4, 0))
-                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], sm + C::O_V, 1, t);
+                att_fp16_rows<D, C::GROUPS>(&c, &a, &pl, &d, s_seen[i & 3], &s_dirty, sm + C::O_V, 1, t);
         };
         auto publish = [&]() {  // operands in shared memory, TMEM reads done: the MMA warp goes on
             fence_async_smem();
@@ -906,6 +957,8 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                     for (int x = 0; x < MH; ++x)
                         st_checked(dst + k * D + 128 * x, o[x][k] * f);
             }
+            if (__builtin_expect(s_dirty, 0))
+                att_add_nonfinite<D, MH>(&a, &d, a.v + ((size_t)d.b * c.H + h) * a.N * D, r0, rows, run16(32 * qd + lane), dst);
         };
 
 #pragma unroll 1

@@ -110,12 +110,11 @@ static __device__ __noinline__ void warp_locate(const kivi_cache* c, const Atten
             w.s = warp_seq(*c, *a, lgG, b);
         total += __reduce_add_sync(0xffffffffu, b < c->B ? w.s.nt * c->H : 0);
     }
-    // A unit a range or more, and 32 ranges a row: past that merging the pieces
-    // costs more than the warps save (four sequences of 8 heads and 69 units:
-    // 17.7 us with a unit each, 16.6 with two or three).
-    count = min(count, total);
-    if (c->B * c->H < count / 32)
-        count = 32 * c->B * c->H;
+    // A unit a range or more, and 40 ranges a row on average: past that merging
+    // the pieces costs more than the warps save (four sequences of 8 heads and
+    // 69 units: 17.7 us with a unit each, 16.6 with two).
+    const unsigned least = total > 0 ? (total - 1) / 40u / (unsigned)(c->B * c->H) + 1 : 1;
+    count = min(count, least > 1 ? (int)((total - 1) / least + 1) : total);
     WarpRange r = {0, 0, 1, 0};
     if (index < count) {
         r.base = (int)((unsigned)total / (unsigned)count);
@@ -250,9 +249,10 @@ static __device__ __noinline__ void warp_fp16_keys(const uint16_t* src, uint8_t*
     cp_async_commit();
     cp_async_wait_all();
 }
-template <int D>
-static __device__ __noinline__ void warp_fp16_values(const uint16_t* src, uint8_t* hat, int lane)
+template <int D, bool DRAFTS>
+static __device__ __noinline__ bool warp_fp16_values(const uint16_t* src, uint8_t* hat, int lane, bool draft)
 {
+    bool cleared = false;
     uint8_t* row = hat + lane * (2 * D);
     const int x = (lane & 7) << 4;
 #pragma unroll 2
@@ -262,7 +262,9 @@ static __device__ __noinline__ void warp_fp16_values(const uint16_t* src, uint8_
             y = ldg_checked(reinterpret_cast<const uint4*>(src + c0));
             z = ldg_checked(reinterpret_cast<const uint4*>(src + c0) + 1);
         }
-        const uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+        uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+        if (DRAFTS && draft)
+            cleared |= clear_nonfinite(q);
         uint32_t o[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -273,6 +275,7 @@ static __device__ __noinline__ void warp_fp16_values(const uint16_t* src, uint8_
         *reinterpret_cast<uint4*>(row + ((c0 * 2) ^ x)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(row + ((c0 * 2 + 16) ^ x)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    return cleared;
 }
 // Four 8 x 8 b16 matrices, not transposed.
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
@@ -280,6 +283,28 @@ __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+// Adds to the M stored rows at dst the values that are not finite of the drafts
+// which they attend.
+template <int D>
+static __device__ __noinline__ void warp_add_nonfinite(const AttendArgs* a, const uint16_t* v, int b, int nd, int M,
+                                                       float* dst, int lane)
+{
+    __syncwarp();  // the rows are stored
+#pragma unroll 1
+    for (int x = lane; x < nd * D; x += 32) {
+        const int j = x / D, ch = x % D;
+        const float y = nonfinite(v + x);
+        if (y == 0.0f)
+            continue;
+#pragma unroll 1
+        for (int row = 0; row < M; ++row) {
+            const int i = row % a->N;
+            if (i < nd && (ldg_checked(a->mask + (size_t)b * a->N + i) >> j) & 1)
+                st_checked(dst + (size_t)row * D + ch, dst[(size_t)row * D + ch] + y);
+        }
+    }
 }
 
 template <int D, int NT, int B>
@@ -293,7 +318,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
     __shared__ uint64_t s_full[C::WARPS][2];
     __shared__ WarpWalk s_walk[C::WARPS];
     __shared__ WarpRange s_range[C::WARPS];
-    __shared__ int s_abort[C::WARPS];
+    __shared__ int s_abort[C::WARPS], s_dirty[C::WARPS];  // dirty: values of some draft were cleared
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int g = lane >> 2, tq = lane & 3;
     // neighbouring ranges on different SMs: few ranges, or the longer ones, are
@@ -303,7 +328,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
     if (lane == 0) {
         mbar_init(&s_full[warp][0], 1);
         mbar_init(&s_full[warp][1], 1);
-        s_abort[warp] = 0;
+        s_abort[warp] = s_dirty[warp] = 0;
         if (index == 0)
             *status = KIVI_OK;
         mbar_fence_init();
@@ -586,7 +611,10 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 default: warp_values<D, B ? B : 8>(stage[1], hat, lane, pl.vub, pl.lgG); break;
                 }
             } else {
-                warp_fp16_values<D>(fp16_src(c.vres, a.v), hat, lane);
+                if (f0 + 32 <= w.s.res)
+                    warp_fp16_values<D, false>(fp16_src(c.vres, a.v), hat, lane, false);
+                else if (warp_fp16_values<D, true>(fp16_src(c.vres, a.v), hat, lane, f0 + lane >= w.s.res))
+                    s_dirty[warp] = 1;
             }
             __syncwarp();
             if (xgo)
@@ -693,6 +721,8 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                     }
                 }
             }
+            if (__builtin_expect(s_dirty[warp], 0))
+                warp_add_nonfinite<D>(&a, a.v + ((size_t)w.b * c.H + w.h) * a.N * D, w.b, w.s.nd, pl.M, dst, lane);
         }
         w = x;
     }

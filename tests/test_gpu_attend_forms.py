@@ -13,6 +13,7 @@ from kivi_bit_kv_gb300 import abi
 from test_gpu_attend import check_sparse, check_tree, run_sparse, run_tree, tree_inputs
 from test_gpu_select import check_select, run_select
 
+NAN = float("nan")
 pytestmark = pytest.mark.gpu
 
 WIDTHS = [(2, 2), (4, 4), (8, 8), (8, 2), (2, 4)]
@@ -95,6 +96,44 @@ def test_long_sparse_batch_keeps_its_precision(cuda):
     # 66 additions a channel rounded to nearest (2^-24 each), 66 truncated units
     # of 8 products (2^-23 each of a 66th of the sum), weights to 2^-21
     assert rel < 66 * 2.0 ** -24 + 8 * 2.0 ** -23 + 2.0 ** -21, rel
+
+
+@pytest.mark.parametrize("D,gq,N", [(64, 1, 6), (128, 2, 5), (128, 1, 14), (128, 1, 20), (64, 2, 30), (128, 1, 60),
+                                    (128, 2, 50), (256, 1, 7), (256, 1, 21)])
+def test_values_that_are_not_finite_reach_only_their_rows(cuda, D, gq, N):
+    """A drafted token whose key or values are NaN or infinite, attended by some
+    rows: the others match the formula without it."""
+    lens = [300, 33]
+    case = (2, 2, 2 * gq, D, 2, 2, 32, 32, lens, N, None)
+    cache = make_cache(cuda, 2, 2, D, 2, 2, 32, 32, lens, seed=80)
+    q, k, v, _, _ = tree_inputs(case, seed=81)
+    rng = np.random.default_rng(82)
+    rows = [[int.from_bytes(rng.bytes(8), "little") & ((1 << N) - 1) for _ in range(N)] for _ in range(2)]
+    jv, jk = N // 3, N - 1
+    v[:, :, jv, 5], v[:, :, jv, D - 1], v[:, :, jv, 20] = NAN, float("inf"), -float("inf")
+    k[:, :, jk, 9] = float("inf")
+    out = run_tree(cache, q, k, v, torch.stack([mask_words(x, N) for x in rows]))
+    K, V = materialized(cache, 0), materialized(cache, 1)
+    seen = 0
+    for b in range(2):
+        for i in range(N):
+            if rows[b][i] >> jk & 1:
+                continue  # an infinite (or NaN) logit: the row is 0 of it, or NaN
+            js = [j for j in range(N) if rows[b][i] >> j & 1 and j != jv]
+            o = out[b, :, i]
+            if not rows[b][i] >> jv & 1:
+                for hq in range(2 * gq):
+                    h = hq // gq
+                    want, bound = attend_ref(q[b, hq, i].double(), torch.cat([K[b, h, :lens[b]], k[b, h, js].double()]),
+                                             torch.cat([V[b, h, :lens[b]], v[b, h, js].double()]), D ** -0.5)
+                    check_rows(o[hq], want, bound, f"b={b} hq={hq} i={i}")
+                continue
+            seen += 1
+            assert torch.isnan(o[:, 5]).all() and (o[:, D - 1] == float("inf")).all()
+            assert (o[:, 20] == -float("inf")).all()
+            rest = [d for d in range(D) if d not in (5, 20, D - 1)]
+            assert torch.isfinite(o[:, rest]).all(), f"b={b} i={i}"
+    assert seen > 0
 
 
 SELECT = {
