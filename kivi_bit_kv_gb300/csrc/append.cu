@@ -151,7 +151,9 @@ __device__ __forceinline__ int path_status(const kivi_cache& c, int L, int n, co
 // where the residual reaches R + G; there the oldest G tokens are flushed as
 // append_kernel flushes them, and the next run reuses their slots.  Bound by
 // latency: a dependent chain of length, path and token loads, then one store
-// (16 x 8 B of D = 128 channels per token and head).
+// (16 x 8 B of D = 128 channels per token and head).  With the second
+// kernel 3.6 us for one small sequence; 13 us for 64 sequences of 32 heads that
+// keep up to eight tokens each, nine of which flush a group (16.5 MB).
 template <int BK, int BV>
 __global__ void __launch_bounds__(128)
 append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int N,

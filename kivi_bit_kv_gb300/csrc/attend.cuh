@@ -59,7 +59,7 @@
 // frees its TMEM and ends.
 //
 // Measured: 128 query rows over four int2 contexts of 32768 tokens and eight KV
-// heads, D = 128: 296 us, 225 TFLOP/s of the two products (66.6 GFLOP) and 139
+// heads, D = 128: 300 us, 222 TFLOP/s of the two products (66.6 GFLOP) and 139
 // MB read once.  The chain of steps between barriers bounds it: the
 // schedulers issue in 56 % of the cycles, 35 instructions per weight, of which
 // six rebuild the operands; the tensor cores are busy 17 % of the time and DRAM

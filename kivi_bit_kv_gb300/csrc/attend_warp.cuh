@@ -33,12 +33,13 @@
 // copies have landed (a bounded wait as well).
 //
 // Measured: one row a KV head over 1024 listed tokens and the residual of 64
-// ragged int2 sequences of 32 heads (418 MB): 158 us, 2.6 TB/s; 8 rows over a
-// 2065-token int4 prefix of 32 x 32 heads (420 MB): 166 us, 2.5 TB/s; 16 rows
-// over eight int2 sequences of 4096 tokens (152 MB): 124 us.  The issue rate
-// bounds it: some 1200 instructions a unit of 4096 elements of K and of V each,
-// at half an instruction a cycle from the four warps that a scheduler's
-// registers hold; deeper unrolling made it slower (instruction fetch).
+// ragged int2 sequences of 32 heads (418 MB): 162 us, 2.6 TB/s; 8 rows over a
+// 2065-token int4 prefix of 32 x 32 heads (420 MB): 172 us, 2.4 TB/s; 16 rows
+// over eight int2 sequences of 4096 tokens (152 MB): 124 us.  Chains of
+// dependent instructions bound it: some 1200 instructions a unit of 4096
+// elements of K and of V each, issued in 52 % of the cycles by the four warps
+// that a scheduler's registers and shared memory hold; ALU and shared memory are
+// busy half of the time.  Deeper unrolling made it slower (instruction fetch).
 #pragma once
 
 #include "attend.cuh"
