@@ -303,6 +303,7 @@ __device__ __forceinline__ void att_next(AttWalk& w, const kivi_cache& c, const 
         if (w.s.nt > 0)
             return;
     }
+    w.b = c.B - 1;  // only if a length was changed meanwhile: stay inside the arrays
 }
 
 // One warp: the CTA's range of tiles [range[0], range[1]) of range[2], one of
@@ -358,6 +359,9 @@ static __device__ __noinline__ void att_locate(const kivi_cache* c, const Attend
         }
         before = __shfl_sync(0xffffffffu, before + inc, 31);
     }
+    // p < total, so only if a length was changed meanwhile
+    if (lane == 0)
+        range[1] = p;
 }
 
 // What the workers need of a tile, written by the copy warp.

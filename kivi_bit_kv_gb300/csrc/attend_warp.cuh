@@ -80,6 +80,7 @@ __device__ __forceinline__ void warp_next(WarpWalk& w, const kivi_cache& c, cons
         if (w.s.nt > 0)
             return;
     }
+    w.b = c.B - 1;  // only if a length was changed meanwhile: stay inside the arrays
 }
 
 // The split of all units into ranges of `base` units, the first `rem` of them
@@ -130,7 +131,7 @@ static __device__ __noinline__ void warp_locate(const kivi_cache* c, const Atten
         return;
     int before = 0;
 #pragma unroll 1
-    for (;;) {
+    for (; w.b - lane < c->B; w.b += 32) {
         if (c->B > 32 && w.b < c->B)  // else as in the first pass
             w.s = warp_seq(*c, *a, lgG, w.b);
         const int n = w.b < c->B ? w.s.nt * c->H : 0;
@@ -141,18 +142,21 @@ static __device__ __noinline__ void warp_locate(const kivi_cache* c, const Atten
             inc += lane >= o ? t : 0;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, r.first < before + inc);
-        if (hit) {  // in the end: first < total
+        if (hit) {
             if (lane == __ffs(hit) - 1) {
                 const unsigned at = r.first - (before + inc - n);
                 w.h = (int)(at / (unsigned)w.s.nt);
                 w.j = (int)(at - (unsigned)w.h * w.s.nt);
                 *first = w;
             }
-            break;
+            __syncwarp();
+            return;
         }
         before = __shfl_sync(0xffffffffu, before + inc, 31);
-        w.b += 32;
     }
+    // first < total, so only if a length was changed meanwhile
+    if (lane == 0)
+        range->n = 0;
     __syncwarp();
 }
 
