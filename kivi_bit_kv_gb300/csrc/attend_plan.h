@@ -127,7 +127,6 @@ constexpr int kWarpStatic = 4 * 1024;                      // bound on its stati
 
 template <int D, int NT>
 struct WarpCfg {
-    static constexpr int NR = 8 * NT;                      // rows
     static constexpr int WARPS = NT == 2 ? 12 : D == 256 ? 10 : 16;  // by registers: 168, 200, 128 a thread
     static constexpr int HAT = 64 * D;                     // K_hat or V_hat of a unit
     static_assert(D != 256 || NT == 1, "registers");

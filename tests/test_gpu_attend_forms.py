@@ -76,6 +76,18 @@ def test_logits_far_outside_fp16(cuda, N):
     assert checked >= N // 2
 
 
+@pytest.mark.parametrize("D,gq", [(256, 16), (256, 9), (256, 8), (128, 16), (64, 9)])
+def test_sparse_skips_bad_entries_in_every_form(cuda, D, gq):
+    """Whole tiles and units of skipped entries, the first ones too."""
+    lens = [1500, 700, 90]
+    cache = make_cache(cuda, 3, 1, D, 4, 2, 32, 32, lens, seed=90)
+    q = f16(torch.Generator().manual_seed(91), 3, gq, D)
+    blocks = torch.full((3, 1, 20), -1, dtype=torch.int32)
+    blocks[0, 0, 9:] = torch.tensor([45, 3, 46, -2 ** 31, 3, 0, 2 ** 31 - 1, 1, 2, 44, 7])
+    blocks[1, 0, ::3] = torch.tensor([20, 21, 0, 5, 5, 5, 19])
+    check_sparse(cache, lens, q, blocks, run_sparse(cache, q, blocks))
+
+
 def test_long_sparse_batch_keeps_its_precision(cuda):
     """Rows whose whole list one warp walks: the error does not grow with the
     length (an accumulation that truncates would lose 2^-23 of the output per
