@@ -34,7 +34,7 @@
 //
 // Measured: one row a KV head over 1024 listed tokens and the residual of 64
 // ragged int2 sequences of 32 heads (418 MB): 162 us, 2.6 TB/s; 8 rows over a
-// 2065-token int4 prefix of 32 x 32 heads (420 MB): 172 us, 2.4 TB/s; 16 rows
+// 2065-token int4 prefix of 32 x 32 heads (420 MB): 169 us, 2.5 TB/s; 16 rows
 // over eight int2 sequences of 4096 tokens (152 MB): 124 us.  Chains of
 // dependent instructions bound it: some 1200 instructions a unit of 4096
 // elements of K and of V each, issued in 52 % of the cycles by the four warps
@@ -632,7 +632,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 // additions: the tensor core truncates, and a chain through every unit
                 // of a long row would lose in one direction.  TG tiles at a time, so
                 // that their products do not wait for one another.
-                constexpr int TG = 2;
+                constexpr int TG = NT == 1 ? 4 : 2;  // 8 int4 rows: 169 us with 4, 172 with 2; 16 rows lack registers
 #pragma unroll
                 for (int t0 = 0; t0 < D / 16; t0 += TG) {
                     uint32_t f[2][TG][4];
