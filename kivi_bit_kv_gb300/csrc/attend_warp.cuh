@@ -744,19 +744,32 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 // Merges the pieces of the rows that ranges cut, piece by piece in order: block
 // i takes row i (few rows, 512 threads: each has many pieces), or the row that
 // starts in range i and ends in a later one (256 threads).
-template <int T>
-__global__ void __launch_bounds__(T)
+//
+// A record by row is written by the range in which its row ends or is cut, so
+// one whose row has no unit (a sequence without drafts) holds whatever the
+// workspace held: the block takes its row from its own index and leaves before
+// it reads one.  Records by range are all written, and name their row.
+template <bool BY_ROW>
+__global__ void __launch_bounds__(BY_ROW ? 512 : 256)
 attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ AttendArgs a, int M,
                            int ranges, float* __restrict__ ws)
 {
+    constexpr int T = BY_ROW ? 512 : 256;
     const int D = c.D;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 cut = reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[blockIdx.x];
-    // a sequence without drafts, or a kernel that gave up, leaves its records as they were
+    int4 cut = reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[blockIdx.x];
+    if (BY_ROW) {
+        cut.z = (int)(blockIdx.x / (unsigned)c.H);
+        cut.w = (int)(blockIdx.x % (unsigned)c.H);
+    }
     const int last = cut.x, i = cut.y, b = cut.z, h = cut.w;
-    if (i < 0 || last <= i || last >= ranges || b < 0 || b >= c.B || h < 0 || h >= c.H)
+    // a kernel that gave up leaves its records as they were: stay inside the arrays
+    const bool merge = i >= 0 && last > i && last < ranges;
+    if (!BY_ROW && !(merge && b >= 0 && b < c.B && h >= 0 && h < c.H))
         return;
     const int nd = a.k ? (a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), a.N) : a.N) : 1;
+    if (BY_ROW && !(merge && nd > 0))
+        return;
     // 64 pieces at a time: their weights (a warp per row, a lane per two pieces),
     // then the weighted sum of their outputs, four channels a thread and the
     // pieces spread over the threads that are left
@@ -882,7 +895,7 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, pl.by_row ? attend_warp_combine_kernel<512> : attend_warp_combine_kernel<256>, c, a,
+    return cudaLaunchKernelEx(&cfg, pl.by_row ? attend_warp_combine_kernel<true> : attend_warp_combine_kernel<false>, c, a,
                               pl.M, N * pl.warps, ws);
 }
 
