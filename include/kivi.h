@@ -298,7 +298,9 @@ int32_t kivi_decode_pv_noalloc(const kivi_cache* c, const float* logits,
  * values that kivi_dequant materializes (K_hat, V_hat = x_hat of the codes,
  * fp16 residual tokens as they are), with fp32 sums and softmax statistics.
  * A sequence's len[b] is read on the device and taken as min(len[b], Tmax)
- * (0 if negative).
+ * (0 if negative).  A row whose softmax is NaN -- a NaN in its query or in a key
+ * that it attends, a logit of +infinity -- is NaN; only a row whose weights are
+ * all zero (nothing to attend, or logits of -infinity alone) is 0.
  */
 
 /* Largest number of drafted tokens of one kivi_tree_attention call. */

@@ -199,6 +199,9 @@ __device__ __forceinline__ void mul_pair(float* x, float f)
 {
     put_pair(x, __fmul2_rn(make_float2(x[0], x[1]), make_float2(f, f)));
 }
+// What a row's output is multiplied by, given the sum of its weights: 0 if it
+// attends nothing.  A NaN sum (a NaN logit, or an infinite one) stays NaN.
+__device__ __forceinline__ float row_scale(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 // p = hi + lo as two fp16 pairs: the upper 11 bits, and what is left of them.
 __device__ __forceinline__ void split_pair(float* p, uint32_t& hi, uint32_t& lo)
 {
@@ -937,7 +940,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
             float *dst, scale = 1.0f;
             bool mine = lane < NC;  // row `lane` is stored
             if (d.tail && !d.mid) {
-                scale = L > 0.0f ? 1.0f / L : 0.0f;
+                scale = row_scale(L);
                 mine = mine && r0 + lane < pl.M && (!a.k || (r0 + lane) % a.N < d.nd);
                 dst = a.out + (((size_t)d.b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + r0) * D;
             } else {
@@ -1203,7 +1206,7 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
             o = o * f + x * g;
             M = Mn;
         }
-        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, L > 0.0f ? o / L : 0.0f);
+        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, L == 0.0f ? 0.0f : o / L);
     }
 }
 

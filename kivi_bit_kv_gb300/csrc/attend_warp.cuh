@@ -692,7 +692,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 dst = a.out + ((size_t)w.b * a.Hq + (size_t)w.h * (a.Hq / c.H)) * a.N * D;
 #pragma unroll
                 for (int k = 0; k < NCOL; ++k)
-                    scale[k] = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
+                    scale[k] = row_scale(l[k]);
                 if (pl.by_row && lane == 0)
                     cuts[w.b * c.H + w.h] = make_int4(-1, 0, 0, 0);
             } else {
@@ -856,7 +856,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     for (int k = 0; k < 2; ++k) {
         const int e4 = t + k * T, r = e4 * 4 / D;
         if (e4 < n4 && r % a.N < nd) {
-            const float inv = s_l[r] > 0.0f ? 1.0f / s_l[r] : 0.0f;
+            const float inv = row_scale(s_l[r]);
             st_checked(reinterpret_cast<float4*>(
                            a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N) * D) + e4,
                        make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
