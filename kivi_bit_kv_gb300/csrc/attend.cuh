@@ -214,8 +214,10 @@ __device__ __forceinline__ void split_pair(float* p, uint32_t& hi, uint32_t& lo)
 // A value that is not finite must not reach the product: its weight of 0 in a
 // row that does not attend its token would still make the row NaN.  The fp16
 // values of drafted tokens are cleared of such halves here (true if there were
-// any), and added to the stored rows that attend them (a row may get one twice,
-// where two pieces of it hold drafts: the sum is the same).
+// any) and added to the stored rows that attend them, once and after the
+// division by the row's sum: a row in one piece by its worker, a cut one by the
+// merge.  A piece says that it cleared some by the sign of its rows' sums (its
+// own weight may be 0, which would make NaN of them).
 __device__ __forceinline__ bool clear_nonfinite(uint32_t (&q)[8])
 {
     uint32_t any = 0;
@@ -640,7 +642,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
     extern __shared__ uint8_t att_smem[];
     __shared__ AttDesc s_desc[kAttDescs];
     __shared__ unsigned long long s_seen[4][4];                // drafts any row attends, by tile
-    __shared__ int s_dirty;                                    // values of some draft were cleared
+    __shared__ int s_dirty;                                    // values of some draft were cleared (of any row tile so far)
     __shared__ __align__(16) float s_red[C::GROUPS][NC][4];            // maxima: [row group][row][lane quadrant]
     __shared__ float s_part[C::GROUPS][128];
     __shared__ __align__(16) float s_ref[C::GROUPS][C::REG_REF ? 1 : NC];
@@ -949,7 +951,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                 const float rf = my_ref();
                 if (qd == 0 && lane < NC) {
                     st_checked(piece + (size_t)NR * D + wg * NC + lane, rf);
-                    st_checked(piece + (size_t)NR * D + NR + wg * NC + lane, L);
+                    st_checked(piece + (size_t)NR * D + NR + wg * NC + lane, copysignf(L, s_dirty ? -1.0f : 1.0f));
                 }
             }
             uint32_t rows = __ballot_sync(0xffffffffu, mine);
@@ -964,7 +966,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                     for (int x = 0; x < MH; ++x)
                         st_checked(dst + k * D + 128 * x, o[x][k] * f);
             }
-            if (__builtin_expect(s_dirty, 0))
+            if (__builtin_expect(s_dirty && d.tail && !d.mid, 0))
                 att_add_nonfinite<D, MH>(&a, &d, a.v + ((size_t)d.b * c.H + h) * a.N * D, r0, rows, run16(32 * qd + lane), dst);
         };
 
@@ -1197,16 +1199,27 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
         if (row >= pl.M || row % a.N >= nd)
             continue;
         float M = kAttNoRef, L = 0.0f, o = 0.0f;
+        bool dirty = false;
 #pragma unroll 1
         for (int k = i; k <= last; ++k) {
             const float* p = att_part(ws, D, NR, k, k == i);
-            const float m = p[(size_t)NR * D + r], l = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
-            const float Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
+            const float m = p[(size_t)NR * D + r], ls = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
+            dirty |= signbit(ls);
+            const float l = fabsf(ls), Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
             L = L * f + l * g;
             o = o * f + x * g;
             M = Mn;
         }
-        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, L == 0.0f ? 0.0f : o / L);
+        o = L == 0.0f ? 0.0f : o / L;
+        if (__builtin_expect(dirty, 0)) {
+            const uint64_t* mw = a.mask + ((size_t)b * a.N + row % a.N) * ((a.N + 63) >> 6);
+            const uint16_t* v = a.v + ((size_t)b * c.H + h) * a.N * D + d;
+#pragma unroll 1
+            for (int j = 0; j < nd; ++j)
+                if ((ldg_checked(mw + (j >> 6)) >> (j & 63)) & 1)
+                    o += nonfinite(v + (size_t)j * D);
+        }
+        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, o);
     }
 }
 

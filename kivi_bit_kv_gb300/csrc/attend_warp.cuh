@@ -290,8 +290,8 @@ __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr));
 }
 
-// Adds to the M stored rows at dst the values that are not finite of the drafts
-// which they attend.
+// Adds to the M rows of output at dst the values that are not finite of the
+// drafts which they attend.
 template <int D>
 static __device__ __noinline__ void warp_add_nonfinite(const AttendArgs* a, const uint16_t* v, int b, int nd, int M,
                                                        float* dst, int lane)
@@ -703,7 +703,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                         const int row = 8 * (k >> 1) + 2 * tq + (k & 1);
                         if (row < pl.M) {
                             dst[pl.M * D + row] = ref[k];
-                            dst[pl.M * D + pl.M + row] = l[k];
+                            dst[pl.M * D + pl.M + row] = copysignf(l[k], s_dirty[warp] ? -1.0f : 1.0f);
                         }
                     }
                 }
@@ -726,7 +726,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                     }
                 }
             }
-            if (__builtin_expect(s_dirty[warp], 0))
+            if (__builtin_expect(s_dirty[warp] && tail && !mid, 0))
                 warp_add_nonfinite<D>(&a, a.v + ((size_t)w.b * c.H + w.h) * a.N * D, w.b, w.s.nd, pl.M, dst, lane);
         }
         w = x;
@@ -776,8 +776,11 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     constexpr int P = 64;
     __shared__ float s_w[16][P], s_m[16], s_l[16], s_f[16];
     __shared__ float4 s_o[T];
+    __shared__ int s_dirty;  // some piece cleared values of drafts
     const int t = threadIdx.x, lane = t & 31, n4 = M * D / 4;
     const int groups = n4 < T ? T / n4 : 1;
+    if (t == 0)
+        s_dirty = 0;
     if (t < M) {
         s_m[t] = -INFINITY;
         s_l[t] = 0.0f;
@@ -799,6 +802,9 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
                 const float* p = warp_part(ws, D, M, k0 + q, k0 + q == i) + M * D + r;
                 m[k] = q < np ? p[0] : -INFINITY;
                 l[k] = q < np ? p[M] : 0.0f;
+                if (__builtin_expect(signbit(l[k]), 0))
+                    s_dirty = 1;
+                l[k] = fabsf(l[k]);
             }
             const float old = s_m[r], mx = fmaxf(old, redux_max(fmaxf(m[0], m[1])));
             float L = 0.0f;
@@ -857,9 +863,22 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
         const int e4 = t + k * T, r = e4 * 4 / D;
         if (e4 < n4 && r % a.N < nd) {
             const float inv = row_scale(s_l[r]);
+            float4 y = make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
+            if (__builtin_expect(s_dirty, 0)) {
+                const uint16_t* v = a.v + ((size_t)b * c.H + h) * a.N * D + e4 * 4 % D;
+                const uint64_t word = ldg_checked(a.mask + (size_t)b * a.N + r % a.N);  // (N <= 16: one a row)
+#pragma unroll 1
+                for (int j = 0; j < nd; ++j) {
+                    if (!((word >> j) & 1))
+                        continue;
+                    y.x += nonfinite(v + j * D);
+                    y.y += nonfinite(v + j * D + 1);
+                    y.z += nonfinite(v + j * D + 2);
+                    y.w += nonfinite(v + j * D + 3);
+                }
+            }
             st_checked(reinterpret_cast<float4*>(
-                           a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N) * D) + e4,
-                       make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+                           a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N) * D) + e4, y);
         }
     }
 }
