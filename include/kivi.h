@@ -316,7 +316,11 @@ int32_t kivi_decode_pv_noalloc(const kivi_cache* c, const float* logits,
  * for the Tq/G quantized groups; entries past them are not written.  The
  * arithmetic is fp32 and its order fixed -- each product rounded, then sums of
  * neighbouring channels, of neighbouring pairs, and so on -- so that scores and
- * choice are the same bit for bit from run to run and on any implementation.
+ * choice are the same bit for bit from run to run and on any implementation
+ * (up to the sign of a zero and the bits of a NaN).  Both maxima are NaN if
+ * either side is: a NaN in a head's query makes every score of its KV head NaN.
+ * (For an infinite q_d the inner maximum is q_d hi_d or q_d lo_d by the sign of
+ * q_d, whatever the other product is.)
  *   blocks[b][h][0 .. n_keep) = the indices of the min(n_keep, Tq/G) groups of
  * largest score, the lower index first among equal scores (a NaN counts as the
  * lowest), in ascending order, then -1.
