@@ -389,8 +389,9 @@ size_t kivi_attend_workspace_bytes(const kivi_cache* c, int32_t Hq, int32_t N);
  * flushes, len[b]).  path: int32 [B][P]; counts: int32 [B]; 1 <= N, P.
  * A sequence is left unchanged and *status (device int32) set if counts[b] is
  * outside [0, P] or one of its path entries outside [0, N) (KIVI_EINVAL), or
- * if it would exceed Tmax (KIVI_ECAPACITY); *status is otherwise not written.
- * The same token may appear twice on a path.  Two kernels on `stream`.
+ * if it would exceed Tmax (KIVI_ECAPACITY); *status is otherwise not written,
+ * and KIVI_EINVAL if a call finds both.  The same token may appear twice on a
+ * path.  Two kernels on `stream`.
  */
 int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k,
                          const uint16_t* v, int32_t N, const int32_t* path,

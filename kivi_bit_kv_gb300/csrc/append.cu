@@ -167,7 +167,7 @@ append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t*
     const int32_t* row = path + (size_t)b * P;
     const int st = path_status(c, L, n, row, N, P);
     if (st != KIVI_OK) {  // uniform over the CTA
-        if (h == 0 && threadIdx.x == 0)
+        if (st == KIVI_ECAPACITY && h == 0 && threadIdx.x == 0)
             atomicExch(status, st);
         return;
     }
@@ -206,10 +206,12 @@ append_path_kernel(kivi_cache c, const uint16_t* __restrict__ k, const uint16_t*
 }
 
 // One warp per sequence: adds the tokens append_path_kernel appended.  Its CTAs
-// start with that kernel's, which read `len`, and write once it has ended.
+// start with that kernel's, which read `len`, and write once it has ended.  That
+// kernel reports full sequences and this one bad arguments, so that the status
+// of a call with both does not depend on which CTA is last.
 __global__ void __launch_bounds__(128)
 advance_path_kernel(kivi_cache c, int N, const int32_t* __restrict__ path, int P,
-                    const int32_t* __restrict__ counts)
+                    const int32_t* __restrict__ counts, int32_t* status)
 {
     const int b = (int)(blockIdx.x * 4 + threadIdx.x / 32);
     if (b >= c.B)
@@ -217,8 +219,12 @@ advance_path_kernel(kivi_cache c, int N, const int32_t* __restrict__ path, int P
     const int L = ld_checked(c.len + b), n = ldg_checked(counts + b);
     const int st = path_status(c, L, n, path + (size_t)b * P, N, P);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (st == KIVI_OK && (threadIdx.x & 31) == 0)
+    if ((threadIdx.x & 31) != 0)
+        return;
+    if (st == KIVI_OK)
         st_checked(c.len + b, L + n);
+    else if (st == KIVI_EINVAL)
+        atomicExch(status, st);
 }
 
 template <int BK>
@@ -257,7 +263,7 @@ cudaError_t launch_append_path(const kivi_cache& c, const uint16_t* k, const uin
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, advance_path_kernel, c, N, path, P, counts);
+    return cudaLaunchKernelEx(&cfg, advance_path_kernel, c, N, path, P, counts, status);
 }
 
 #ifdef KIVI_CHECKS
