@@ -377,8 +377,10 @@ int32_t kivi_tree_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq,
                             size_t ws_bytes, void* stream);
 
 /*
- * Workspace bytes of kivi_tree_attention for N drafted tokens and, with N = 1,
- * of kivi_sparse_attention.  Host only; 0 for invalid sizes.
+ * Workspace bytes of kivi_tree_attention for N drafted tokens or fewer and, with
+ * any N, of kivi_sparse_attention: a loop needs one of its largest draft.  The
+ * size depends on D, Hq/H and N, not on B, H or the lengths, and a workspace may
+ * serve several caches in turn.  Host only; 0 for invalid sizes.
  */
 size_t kivi_attend_workspace_bytes(const kivi_cache* c, int32_t Hq, int32_t N);
 

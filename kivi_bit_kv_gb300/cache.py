@@ -60,7 +60,7 @@ class KiviCache:
         return torch.empty((max(n, 16) + 15) // 16 * 4, dtype=torch.float32, device=self.device)
 
     def attend_workspace(self, Hq: int, N: int = 1) -> torch.Tensor:
-        """A workspace for ``kivi_tree_attention`` with N drafted tokens per
-        sequence, or (N = 1) for ``kivi_sparse_attention``."""
+        """A workspace for ``kivi_tree_attention`` with up to N drafted tokens
+        per sequence, and for ``kivi_sparse_attention``."""
         n = abi.kivi_attend_workspace_bytes(self, Hq, N)
         return torch.empty((max(n, 16) + 15) // 16 * 4, dtype=torch.float32, device=self.device)

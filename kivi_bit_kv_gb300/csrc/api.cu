@@ -379,7 +379,7 @@ size_t kivi_attend_workspace_bytes(const kivi_cache* c, int32_t Hq, int32_t N)
 {
     if (check_sizes(c) != KIVI_OK || check_heads(c, Hq) != KIVI_OK || N < 1 || N > KIVI_MAX_DRAFT)
         return 0;
-    return kivi::attend_ws_bytes(*c, Hq, N);
+    return kivi::attend_ws_bytes_upto(*c, Hq, N);
 }
 
 static int32_t check_attend_ws(const kivi_cache* c, int32_t Hq, int32_t N, const float* out, const void* ws,

@@ -14,6 +14,16 @@ size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N)
     return (kAttHeaderFloats + pieces * (kAttCutInts + 2 * floats)) * sizeof(float);
 }
 
+size_t attend_ws_bytes_upto(const kivi_cache& c, int Hq, int N)
+{
+    // the warp kernel has more and smaller pieces than the tcgen05 kernel, so a
+    // call for more drafts may need less
+    size_t most = 0;
+    for (int n = 1; n <= N; ++n)
+        most = attend_ws_bytes(c, Hq, n) > most ? attend_ws_bytes(c, Hq, n) : most;
+    return most;
+}
+
 template <int D>
 static cudaError_t launch_attend_d(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
 {

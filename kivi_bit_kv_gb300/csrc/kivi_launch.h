@@ -66,7 +66,9 @@ cudaError_t launch_attend(const kivi_cache& c, const AttendArgs& a, void* ws, cu
 // instantiated in attend_d<D>_*.cu.
 template <int D, int B>
 cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s);
+// Workspace bytes of a call with N drafted tokens, and of any with up to N.
 size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N);
+size_t attend_ws_bytes_upto(const kivi_cache& c, int Hq, int N);
 cudaError_t launch_decode_qk(const kivi_cache& c, const uint16_t* q, int Hq, float sm_scale,
                              float* logits, int ld_logits, cudaStream_t s);
 // ws_o: [B*Hq][nchunks][D], ws_m / ws_l: [B*Hq][nchunks] (fp32).
