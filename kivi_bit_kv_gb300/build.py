@@ -20,7 +20,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkivi.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
+# -fno-gnu-unique: a launcher template's static (what it has set up for its
+# kernel) stays its library's own; as a unique symbol it would be shared by all
+# copies and variants of the library in a process.
+NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-Xcompiler", "-fno-gnu-unique",
               "-prec-div=true", "-ftz=false", "-prec-sqrt=true",
               f"-I{INCLUDE}", f"-I{CSRC}"]
 
