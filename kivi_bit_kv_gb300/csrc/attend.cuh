@@ -1182,8 +1182,35 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
 // piece by piece in order.
 constexpr int kAttCombineThreads = 256;
 constexpr int kAttCombineRows = 8;
+
+// Adds to this block's rows of the row tile that starts with row `row0` and has
+// `rows` rows the values that are not finite of the drafts which they attend.  A
+// thread takes the elements that it stored.
+static __device__ __noinline__ void att_merge_nonfinite(const kivi_cache* c, const AttendArgs* a, int b, int h, int nd,
+                                                        int row0, int rows)
+{
+    const int D = c->D, W = (a->N + 63) >> 6;
+    const uint16_t* v = a->v + ((size_t)b * c->H + h) * a->N * D;
+    float* dst = a->out + (((size_t)b * a->Hq + (size_t)h * (a->Hq / c->H)) * a->N + row0) * D;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < kAttCombineRows * D; e += kAttCombineThreads) {
+        const int r = blockIdx.y * kAttCombineRows + e / D, d = e % D, q = (row0 + r) % a->N;
+        if (r >= rows || q >= nd)
+            continue;
+        const uint64_t* words = a->mask + ((size_t)b * a->N + q) * W;
+        float y = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < nd; ++j)
+            if ((ldg_checked(words + (j >> 6)) >> (j & 63)) & 1)
+                y += nonfinite(v + (size_t)j * D + d);
+        if (y != 0.0f)
+            st_checked(dst + (size_t)r * D + d, dst[(size_t)r * D + d] + y);
+    }
+}
+
 static __global__ void __launch_bounds__(kAttCombineThreads)
-attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, int NR, float* __restrict__ ws)
+attend_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ AttendArgs a,
+                      const __grid_constant__ AttPlan pl, int NR, float* __restrict__ ws)
 {
     const int D = c.D, i = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1193,34 +1220,32 @@ attend_combine_kernel(const kivi_cache c, const AttendArgs a, const AttPlan pl, 
     const int b = cut[1], rr = cut[2], last = cut[3];
     const int h = rr / pl.RT, rt = rr - h * pl.RT;
     const int nd = a.k ? (a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), a.N) : a.N) : 1;
+    // negative: a piece cleared values of drafts, which lie in the last three tiles
+    int sign[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int piece = max(last - k, i);
+        sign[k] = __float_as_int(att_part(ws, D, NR, piece, piece == i)[(size_t)NR * D + NR]);
+    }
 #pragma unroll 1
     for (int e = threadIdx.x; e < kAttCombineRows * D; e += kAttCombineThreads) {
         const int r = blockIdx.y * kAttCombineRows + e / D, d = e % D, row = rt * NR + r;
         if (row >= pl.M || row % a.N >= nd)
             continue;
         float M = kAttNoRef, L = 0.0f, o = 0.0f;
-        bool dirty = false;
 #pragma unroll 1
         for (int k = i; k <= last; ++k) {
             const float* p = att_part(ws, D, NR, k, k == i);
-            const float m = p[(size_t)NR * D + r], ls = p[(size_t)NR * D + NR + r], x = p[(size_t)r * D + d];
-            dirty |= signbit(ls);
-            const float l = fabsf(ls), Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
+            const float m = p[(size_t)NR * D + r], l = fabsf(p[(size_t)NR * D + NR + r]), x = p[(size_t)r * D + d];
+            const float Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
             L = L * f + l * g;
             o = o * f + x * g;
             M = Mn;
         }
-        o = L == 0.0f ? 0.0f : o / L;
-        if (__builtin_expect(dirty, 0)) {
-            const uint64_t* mw = a.mask + ((size_t)b * a.N + row % a.N) * ((a.N + 63) >> 6);
-            const uint16_t* v = a.v + ((size_t)b * c.H + h) * a.N * D + d;
-#pragma unroll 1
-            for (int j = 0; j < nd; ++j)
-                if ((ldg_checked(mw + (j >> 6)) >> (j & 63)) & 1)
-                    o += nonfinite(v + (size_t)j * D);
-        }
-        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, o);
+        st_checked(a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N + row) * D + d, L == 0.0f ? 0.0f : o / L);
     }
+    if (__builtin_expect((sign[0] | sign[1] | sign[2]) < 0, 0))
+        att_merge_nonfinite(&c, &a, b, h, nd, rt * NR, min(NR, pl.M - rt * NR));
 }
 
 // ----------------------------------------------------------------- launch ---

@@ -741,9 +741,34 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
     }
 }
 
+// Adds to the stored output of row (b, h), M query rows, the values that are
+// not finite of the drafts which they attend.  All threads of the block.
+static __device__ __noinline__ void warp_merge_nonfinite(const kivi_cache* c, const AttendArgs* a, int b, int h, int nd,
+                                                         int M)
+{
+    const int D = c->D;
+    float* dst = a->out + ((size_t)b * a->Hq + (size_t)h * M / a->N) * a->N * D;
+    const uint16_t* v = a->v + ((size_t)b * c->H + h) * a->N * D;
+    __syncthreads();  // the row is stored
+#pragma unroll 1
+    for (int x = threadIdx.x; x < M * D; x += blockDim.x) {
+        const int i = x / D % a->N, ch = x % D;
+        if (i >= nd)
+            continue;
+        const uint64_t word = ldg_checked(a->mask + (size_t)b * a->N + i);  // (N <= 16 here: one word a row)
+        float y = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < nd; ++j)
+            if ((word >> j) & 1)
+                y += nonfinite(v + j * D + ch);
+        if (y != 0.0f)
+            st_checked(dst + x, dst[x] + y);
+    }
+}
+
 // Merges the pieces of the rows that ranges cut, piece by piece in order: block
-// i takes row i (few rows, 512 threads: each has many pieces), or the row that
-// starts in range i and ends in a later one (256 threads).
+// (h, b) takes row (b, h) (few rows, 512 threads: each has many pieces), or
+// block i the row that starts in range i and ends in a later one (256 threads).
 //
 // A record by row is written by the range in which its row ends or is cut, so
 // one whose row has no unit (a sequence without drafts) holds whatever the
@@ -757,12 +782,9 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     constexpr int T = BY_ROW ? 512 : 256;
     const int D = c.D;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int4 cut = reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[blockIdx.x];
-    if (BY_ROW) {
-        cut.z = (int)(blockIdx.x / (unsigned)c.H);
-        cut.w = (int)(blockIdx.x % (unsigned)c.H);
-    }
-    const int last = cut.x, i = cut.y, b = cut.z, h = cut.w;
+    const int4 cut =
+        reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[BY_ROW ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x];
+    const int last = cut.x, i = cut.y, b = BY_ROW ? blockIdx.y : cut.z, h = BY_ROW ? blockIdx.x : cut.w;
     // a kernel that gave up leaves its records as they were: stay inside the arrays
     const bool merge = i >= 0 && last > i && last < ranges;
     if (!BY_ROW && !(merge && b >= 0 && b < c.B && h >= 0 && h < c.H))
@@ -776,11 +798,9 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     constexpr int P = 64;
     __shared__ float s_w[16][P], s_m[16], s_l[16], s_f[16];
     __shared__ float4 s_o[T];
-    __shared__ int s_dirty;  // some piece cleared values of drafts
     const int t = threadIdx.x, lane = t & 31, n4 = M * D / 4;
     const int groups = n4 < T ? T / n4 : 1;
-    if (t == 0)
-        s_dirty = 0;
+    bool dirty = false;  // some piece cleared values of drafts
     if (t < M) {
         s_m[t] = -INFINITY;
         s_l[t] = 0.0f;
@@ -792,6 +812,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
 #pragma unroll 1
     for (int k0 = i; k0 <= last; k0 += P) {
         const int np = min(P, last + 1 - k0);
+        bool cleared = false;
         __syncthreads();
 #pragma unroll 1
         for (int r = t >> 5; r < M; r += T / 32) {
@@ -802,8 +823,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
                 const float* p = warp_part(ws, D, M, k0 + q, k0 + q == i) + M * D + r;
                 m[k] = q < np ? p[0] : -INFINITY;
                 l[k] = q < np ? p[M] : 0.0f;
-                if (__builtin_expect(signbit(l[k]), 0))
-                    s_dirty = 1;
+                cleared |= signbit(l[k]);
                 l[k] = fabsf(l[k]);
             }
             const float old = s_m[r], mx = fmaxf(old, redux_max(fmaxf(m[0], m[1])));
@@ -825,7 +845,7 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
             }
             __syncwarp();
         }
-        __syncthreads();
+        dirty |= __syncthreads_or(cleared);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int e4 = (t + k * T) % (groups * n4) % n4, grp = groups > 1 ? t / n4 : 0;
@@ -863,24 +883,13 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
         const int e4 = t + k * T, r = e4 * 4 / D;
         if (e4 < n4 && r % a.N < nd) {
             const float inv = row_scale(s_l[r]);
-            float4 y = make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
-            if (__builtin_expect(s_dirty, 0)) {
-                const uint16_t* v = a.v + ((size_t)b * c.H + h) * a.N * D + e4 * 4 % D;
-                const uint64_t word = ldg_checked(a.mask + (size_t)b * a.N + r % a.N);  // (N <= 16: one a row)
-#pragma unroll 1
-                for (int j = 0; j < nd; ++j) {
-                    if (!((word >> j) & 1))
-                        continue;
-                    y.x += nonfinite(v + j * D);
-                    y.y += nonfinite(v + j * D + 1);
-                    y.z += nonfinite(v + j * D + 2);
-                    y.w += nonfinite(v + j * D + 3);
-                }
-            }
             st_checked(reinterpret_cast<float4*>(
-                           a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N) * D) + e4, y);
+                           a.out + (((size_t)b * a.Hq + (size_t)h * (a.Hq / c.H)) * a.N) * D) + e4,
+                       make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
         }
     }
+    if (__builtin_expect(dirty, 0))
+        warp_merge_nonfinite(&c, &a, b, h, nd, M);
 }
 
 // ----------------------------------------------------------------- launch ---
@@ -906,7 +915,7 @@ cudaError_t attend_warp_launch(const kivi_cache& c, const AttendArgs& a, float* 
         return e;
     // the combine's CTAs are scheduled while the attention drains
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pl.by_row ? c.B * c.H : N * pl.warps);
+    cfg.gridDim = pl.by_row ? dim3(c.H, c.B) : dim3(N * pl.warps);
     cfg.blockDim = dim3(pl.by_row ? 512 : 256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
