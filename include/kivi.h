@@ -311,7 +311,8 @@ int32_t kivi_decode_pv_noalloc(const kivi_cache* c, const float* logits,
  * key are its statistics, lo_d = zero_d and hi_d = zero_d + M scale_d (an fp32
  * product, then an fp32 sum), so
  *   bound(hq, g) = sum_d max(q_d lo_d, q_d hi_d)
- * is at least q . K_hat_t for every token t of group g, and no codes are read.
+ * is at least q . K_hat_t for every token t of group g, up to the rounding of
+ * these fp32 products and sums and of K_hat to fp16, and no codes are read.
  *   scores[b][h][g] = max over the Hq/H query heads of KV head h of bound
  * for the Tq/G quantized groups; entries past them are not written.  The
  * arithmetic is fp32 and its order fixed -- each product rounded, then sums of

@@ -338,7 +338,7 @@ def _call(fn, where: str, device, *args):
 def kivi_block_select(cache, q: torch.Tensor, blocks: torch.Tensor, scores: torch.Tensor, stream=None):
     """blocks int32 [B, H, n_keep] <- the quantized key groups of largest score,
     ascending and padded with -1; scores fp32 [B, H, Tmax/G] <- the scores, an
-    upper bound of q . k over each group; q fp16 [B, Hq, D] (or [B, Hq, 1, D])."""
+    upper bound of q . k over each group up to rounding; q fp16 [B, Hq, D] (or [B, Hq, 1, D])."""
     B, H, D, dev = cache.B, cache.H, cache.D, cache.device
     Hq = q.shape[1] if q.dim() > 1 else 0
     if q.shape != (B, Hq, D) and q.shape != (B, Hq, 1, D):

@@ -371,7 +371,7 @@ static __device__ __noinline__ void att_locate(const kivi_cache* c, const Attend
 
 // What the workers need of a tile, written by the copy warp.
 struct AttDesc {
-    int b, rr, v0;            // v0: its first virtual token
+    int b, rr;
     int nuq;                  // 32-token units of quantized tokens, 0 .. 4
     int f0;                   // fp16 token (residual, then drafts) at position 0 of the tile; negative before them
     int Tq, res, nd;
@@ -738,7 +738,6 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                         AttDesc& d = s_desc[i & (kAttDescs - 1)];
                         d.b = w.b;
                         d.rr = w.rr;
-                        d.v0 = v0;
                         d.nuq = nuq;
                         d.f0 = v0 - w.s.nq;
                         d.Tq = w.s.Tq;

@@ -7,11 +7,21 @@
 namespace kivi {
 
 // Up to 16 query rows of a KV head (8 at D = 256) go to the warp kernel, more
-// to the tcgen05 kernel, whose products cost the same up to 32 rows.  Both
-// sides, when the tcgen05 kernel had a 16-row tile: 1 row of 64 ragged
-// sequences 168 against 303 us, 8 rows of an int4 prefix 170 against 263, 16
-// rows of eight sequences 126 against 128.  Beyond, the warp kernel would need
-// the registers of 24 rows' O.
+// to the tcgen05 kernel, whose products cost the same up to 32 rows.  Beyond,
+// the warp kernel would need the registers of 24 rows' O (16 at D = 256).  Both
+// sides in us, warp kernel against tcgen05 kernel, int2:
+//     rows of a KV head                     1           8         16
+//     B 8, H 32, D 128, T 4096      77 / 165    82 / 172  124 / 176
+//     B 4, H 8, D 128, T 32768     107 / 161   113 / 171  157 / 173
+//     B 1, H 8, D 128, T 2048       17 /  25    21 /  41   28 /  41
+//     B 1, H 1, D 128, T 32768      73 / 103    78 / 315  113 / 310
+//     B 1, H 8, D 128, T 32768      79 /  66    84 / 100  122 / 101
+//     B 8, H 32, D 64, T 4096       47 / 119    50 / 125   63 / 129
+//     B 8, H 32, D 256, T 4096     193 / 229   200 / 241
+//     B 1, H 8, D 256, T 32768     148 /  74   157 / 113
+// The rule goes by rows alone.  Where few long rows fill neither kernel (the
+// fifth and the last line) the other side is faster: the warp kernel takes
+// ranges longer than it would need to (warp_locate).
 template <int D, int B>
 cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws, cudaStream_t s)
 {

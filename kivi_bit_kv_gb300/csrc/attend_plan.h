@@ -27,7 +27,14 @@ constexpr float kAttLimit = 15.9f;            // ... and stays below 2^15.9, ins
 // whose registers hold O of 16 rows (8 at D = 256).
 inline bool attend_by_warp(int D, int M) { return M <= (D == 256 ? 8 : 16); }
 
-// Rows per row tile of the tcgen05 kernel (attend.cuh) for M query rows.
+// Rows per row tile of the tcgen05 kernel (attend.cuh) for M query rows: the
+// smallest tile that holds them, up to 128; shared memory holds 32 at D = 256.
+// In us with tiles of 32 / 64 / 128 rows, B 8, H 32, T 4096, int2:
+//     M             48                65               128               256
+//     D 128  340/233/315       495/426/324       659/447/349      1443/948/749
+//     D 64   243/199/281       354/364/284       480/382/301      1079/802/642
+// and past 128 rows the whole tiles of 128 are the same or better too, but for
+// one sequence of few heads (160 rows, B 1, H 8, T 32768: 211/173/184).
 inline int attend_rows(int D, int M) { return M <= 32 || D == 256 ? 32 : M <= 64 ? 64 : 128; }
 
 // Workspace: header (status word), a cut descriptor per CTA, two partial

@@ -114,7 +114,9 @@ static __device__ __noinline__ void warp_locate(const kivi_cache* c, const Atten
     }
     // A unit a range or more, and 40 ranges a row on average: past that merging
     // the pieces costs more than the warps save (four sequences of 8 heads and
-    // 69 units: 17.7 us with a unit each, 16.6 with two).
+    // 69 units: 17.7 us with a unit each, 16.6 with two).  For few rows that are
+    // long it is too few: the ranges of one sequence of 32768 tokens have 26 units
+    // (8 query rows: 78 us with one KV head, 84 with eight).
     const unsigned least = total > 0 ? (total - 1) / 40u / (unsigned)(c->B * c->H) + 1 : 1;
     count = min(count, least > 1 ? (int)((total - 1) / least + 1) : total);
     WarpRange r = {0, 0, 1, 0};

@@ -394,10 +394,14 @@ cudaError_t launch_block_select(const kivi_cache& c, const uint16_t* q, int Hq, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    // A warp's registers hold a row of up to 512 groups.  With more rows than the
-    // CTAs of one wave a warp a row takes less of the machine (2048 rows: 14
-    // against 23 us), with fewer a CTA a row is sooner done (4 rows: 8.4 against
-    // 6.8 us).
+    // A warp's registers hold a row of up to 512 groups.  With many rows a warp a
+    // row takes less of the machine, with few a CTA a row is sooner done.  Both
+    // kernels in us, a warp against a CTA a row, D = 128:
+    //     rows             4          608         640        2048
+    //     64 groups    9.2/7.2   17.7/13.3   16.1/17.9   38.3/46.3
+    //     256 groups  11.9/7.5   39.4/32.7   41.2/37.5   94.4/99.7
+    //     500 groups  15.7/7.9   66.4/55.1   68.6/61.5   170/172
+    // The border, four rows an SM, is the one of short rows.
     if (NB <= PickWarp::T * PickWarp::K && BH > 4 * sm_count()) {
         cfg.blockDim = dim3(PickWarp::T);
         return cudaLaunchKernelEx(&cfg, block_pick_kernel<PickWarp>, c, (const float*)scores, blocks, n_keep);
