@@ -624,7 +624,7 @@ static __device__ __noinline__ void att_add_nonfinite(const AttendArgs* a, const
         for (uint32_t left = rows; left; left &= left - 1) {
             const int k = __ffs(left) - 1, i = (r0 + k) % a->N;
             if (i < d->nd && (ldg_checked(a->mask + ((size_t)d->b * a->N + i) * W + (j >> 6)) >> (j & 63)) & 1)
-                st_checked(dst + k * D + half, dst[k * D + half] + y);
+                st_checked(dst + k * D + half, ld_checked(dst + k * D + half) + y);
         }
     }
 }
@@ -665,7 +665,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
         if (lane == 0) {
             s_abort = s_never = s_dirty = 0;
             if (cta == 0)
-                *status = KIVI_OK;
+                st_checked(status, KIVI_OK);
             for (int i = 0; i < pl.ns; ++i) {
                 for (int x = 0; x < 2; ++x) {
                     mbar_init(&s_full[x][i], 1);
@@ -698,7 +698,7 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
         const int b0 = w.b, rr0 = w.rr;
         int* cut = reinterpret_cast<int*>(ws + kAttHeaderFloats) + (size_t)cta * kAttCutInts;
         if (warp == kCopyWarp && lane == 0)
-            cut[0] = 0;
+            st_checked(cut, 0);
         // a unit: 32 tokens' codes, then its scales, then its zeros, at these
         // byte strides per 32 tokens (keys: statistics per group)
         const uint32_t code = which == 0 ? pl.kub : pl.vub;
@@ -752,10 +752,10 @@ attend_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__ Atte
                             // the row tile starts in this range and its last tile, end - 1, is in range
                             // `last`: the first with total (last + 1) / count >= end
                             const long long end = s_range[1] + (w.s.nt - 1 - w.j);
-                            cut[1] = w.b;
-                            cut[2] = w.rr;
-                            cut[3] = (int)((end * s_range[3] + s_range[2] - 1) / s_range[2] - 1);
-                            cut[0] = 1;
+                            st_checked(cut + 1, w.b);
+                            st_checked(cut + 2, w.rr);
+                            st_checked(cut + 3, (int)((end * s_range[3] + s_range[2] - 1) / s_range[2] - 1));
+                            st_checked(cut, 1);
                         }
                     }
                     mbar_arrive_tx(bar, __popc(pmask) * (code + 2 * stat));
@@ -1203,7 +1203,7 @@ static __device__ __noinline__ void att_merge_nonfinite(const kivi_cache* c, con
             if ((ldg_checked(words + (j >> 6)) >> (j & 63)) & 1)
                 y += nonfinite(v + (size_t)j * D + d);
         if (y != 0.0f)
-            st_checked(dst + (size_t)r * D + d, dst[(size_t)r * D + d] + y);
+            st_checked(dst + (size_t)r * D + d, ld_checked(dst + (size_t)r * D + d) + y);
     }
 }
 
@@ -1214,9 +1214,9 @@ attend_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constan
     const int D = c.D, i = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int* cut = reinterpret_cast<const int*>(ws + kAttHeaderFloats) + (size_t)i * kAttCutInts;
-    if (cut[0] == 0)
+    if (ld_checked(cut) == 0)
         return;
-    const int b = cut[1], rr = cut[2], last = cut[3];
+    const int b = ld_checked(cut + 1), rr = ld_checked(cut + 2), last = ld_checked(cut + 3);
     const int h = rr / pl.RT, rt = rr - h * pl.RT;
     const int nd = a.k ? (a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), a.N) : a.N) : 1;
     // negative: a piece cleared values of drafts, which lie in the last three tiles
@@ -1224,7 +1224,7 @@ attend_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constan
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         const int piece = max(last - k, i);
-        sign[k] = __float_as_int(att_part(ws, D, NR, piece, piece == i)[(size_t)NR * D + NR]);
+        sign[k] = __float_as_int(ld_checked(att_part(ws, D, NR, piece, piece == i) + (size_t)NR * D + NR));
     }
 #pragma unroll 1
     for (int e = threadIdx.x; e < kAttCombineRows * D; e += kAttCombineThreads) {
@@ -1235,7 +1235,8 @@ attend_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_constan
 #pragma unroll 1
         for (int k = i; k <= last; ++k) {
             const float* p = att_part(ws, D, NR, k, k == i);
-            const float m = p[(size_t)NR * D + r], l = fabsf(p[(size_t)NR * D + NR + r]), x = p[(size_t)r * D + d];
+            const float m = ld_checked(p + (size_t)NR * D + r), l = fabsf(ld_checked(p + (size_t)NR * D + NR + r)),
+                        x = ld_checked(p + (size_t)r * D + d);
             const float Mn = fmaxf(M, m), f = ex2_ftz(M - Mn), g = ex2_ftz(m - Mn);
             L = L * f + l * g;
             o = o * f + x * g;

@@ -309,7 +309,7 @@ static __device__ __noinline__ void warp_add_nonfinite(const AttendArgs* a, cons
         for (int row = 0; row < M; ++row) {
             const int i = row % a->N;
             if (i < nd && (ldg_checked(a->mask + (size_t)b * a->N + i) >> j) & 1)
-                st_checked(dst + (size_t)row * D + ch, dst[(size_t)row * D + ch] + y);
+                st_checked(dst + (size_t)row * D + ch, ld_checked(dst + (size_t)row * D + ch) + y);
         }
     }
 }
@@ -337,14 +337,14 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
         mbar_init(&s_full[warp][1], 1);
         s_abort[warp] = s_dirty[warp] = 0;
         if (index == 0)
-            *status = KIVI_OK;
+            st_checked(status, KIVI_OK);
         mbar_fence_init();
     }
     warp_locate(&c, &a, pl.lgG, index, count, &s_range[warp], &s_walk[warp]);
     const int n = s_range[warp].n;
     int4* cuts = reinterpret_cast<int4*>(ws + kAttHeaderFloats);
     if (!pl.by_row && lane == 0)
-        cuts[index] = make_int4(-1, 0, 0, 0);
+        st_checked(cuts + index, make_int4(-1, 0, 0, 0));
     asm volatile("griddepcontrol.launch_dependents;");
     if (n == 0)
         return;
@@ -696,7 +696,7 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                 for (int k = 0; k < NCOL; ++k)
                     scale[k] = row_scale(l[k]);
                 if (pl.by_row && lane == 0)
-                    cuts[w.b * c.H + w.h] = make_int4(-1, 0, 0, 0);
+                    st_checked(cuts + w.b * c.H + w.h, make_int4(-1, 0, 0, 0));
             } else {
                 dst = warp_part(ws, D, pl.M, index, mid ? 0 : 1);
                 if (g == 0) {
@@ -704,16 +704,16 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
                     for (int k = 0; k < NCOL; ++k) {
                         const int row = 8 * (k >> 1) + 2 * tq + (k & 1);
                         if (row < pl.M) {
-                            dst[pl.M * D + row] = ref[k];
-                            dst[pl.M * D + pl.M + row] = copysignf(l[k], s_dirty[warp] ? -1.0f : 1.0f);
+                            st_checked(dst + pl.M * D + row, ref[k]);
+                            st_checked(dst + pl.M * D + pl.M + row, copysignf(l[k], s_dirty[warp] ? -1.0f : 1.0f));
                         }
                     }
                 }
                 if (!tail && !mid && lane == 0) {
                     // the row starts in this range; where its last unit lies
                     const WarpRange& r = s_range[warp];
-                    cuts[pl.by_row ? w.b * c.H + w.h : index] =
-                        make_int4(r.of(r.first + n - 1 + (w.s.nt - 1 - w.j)), index, w.b, w.h);
+                    st_checked(cuts + (pl.by_row ? w.b * c.H + w.h : index),
+                               make_int4(r.of(r.first + n - 1 + (w.s.nt - 1 - w.j)), index, w.b, w.h));
                 }
             }
 #pragma unroll
@@ -764,7 +764,7 @@ static __device__ __noinline__ void warp_merge_nonfinite(const kivi_cache* c, co
             if ((word >> j) & 1)
                 y += nonfinite(v + j * D + ch);
         if (y != 0.0f)
-            st_checked(dst + x, dst[x] + y);
+            st_checked(dst + x, ld_checked(dst + x) + y);
     }
 }
 
@@ -784,8 +784,8 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
     constexpr int T = BY_ROW ? 512 : 256;
     const int D = c.D;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 cut =
-        reinterpret_cast<const int4*>(ws + kAttHeaderFloats)[BY_ROW ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x];
+    const int4 cut = ld_checked(reinterpret_cast<const int4*>(ws + kAttHeaderFloats) +
+                                (BY_ROW ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x));
     const int last = cut.x, i = cut.y, b = BY_ROW ? blockIdx.y : cut.z, h = BY_ROW ? blockIdx.x : cut.w;
     // a kernel that gave up leaves its records as they were: stay inside the arrays
     const bool merge = i >= 0 && last > i && last < ranges;
@@ -823,8 +823,8 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
             for (int k = 0; k < 2; ++k) {
                 const int q = lane + 32 * k;
                 const float* p = warp_part(ws, D, M, k0 + q, k0 + q == i) + M * D + r;
-                m[k] = q < np ? p[0] : -INFINITY;
-                l[k] = q < np ? p[M] : 0.0f;
+                m[k] = q < np ? ld_checked(p) : -INFINITY;
+                l[k] = q < np ? ld_checked(p + M) : 0.0f;
                 cleared |= signbit(l[k]);
                 l[k] = fabsf(l[k]);
             }
@@ -858,7 +858,8 @@ attend_warp_combine_kernel(const __grid_constant__ kivi_cache c, const __grid_co
             float4 x = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
 #pragma unroll 8
             for (int q = grp; q < np; q += groups) {
-                const float4 v = *reinterpret_cast<const float4*>(warp_part(ws, D, M, k0 + q, k0 + q == i) + 4 * e4);
+                const float4 v =
+                    ld_checked(reinterpret_cast<const float4*>(warp_part(ws, D, M, k0 + q, k0 + q == i) + 4 * e4));
                 const float wq = s_w[r][q];
                 x.x = fmaf(v.x, wq, x.x);
                 x.y = fmaf(v.y, wq, x.y);
