@@ -491,43 +491,60 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
             if (xgo)
                 issue(0);
 
-            // S^T: tokens 16 m + g (+ 8), rows 8 nt + 2 tq (+ 1)
+            // S^T: tokens 16 m + g (+ 8), rows 8 nt + 2 tq (+ 1).  The tensor core
+            // truncates its sums: a chain of n steps of 16 channels loses some (n + 1) / 2
+            // units of 2^-23 of its sum, 8.5 with all of D = 256 in one, 2.5 in chains
+            // of 64 channels that are added with rounding (the same time: 197 and 203 us
+            // for 1 and 8 rows of B 8, H 32, T 4096).  D = 128 keeps one chain, 4.5
+            // units: two cost 1 % there.
             float s[2][NT][4];
+            auto scores = [&](auto&& load) {
+                constexpr int KC = D == 256 ? 4 : D / 16;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+                for (int k0 = 0; k0 < D / 16; k0 += KC) {
+                    float y[2][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s[m][nt][k] = 0.0f;
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                y[m][nt][k] = 0.0f;
+#pragma unroll
+                    for (int k = k0; k < k0 + KC; ++k)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t f[4];
+                            load(f, k, m);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(y[m][nt], f[0], f[1], f[2], f[3], q[k][nt][0], q[k][nt][1]);
+                        }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2) {
+                                if (k0 == 0) {
+                                    s[m][nt][k] = y[m][nt][k];
+                                    s[m][nt][k + 1] = y[m][nt][k + 1];
+                                } else {
+                                    add_pair(s[m][nt] + k, y[m][nt] + k);
+                                }
+                            }
+                }
+            };
             if (__builtin_expect(!go, 0)) {
                 // fp16 keys: blocks token + 8 (lane / 8) % 2, channel chunk lane / 16
                 const int tok = (lane & 7) + (lane & 8), ck = lane >> 4;
                 const uint32_t at = smem_addr(hat) + tok * (2 * D), sw = (tok & 7) << 4;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t f[4];
-                        ldsm_x4(f, at + m * (32 * D) + (((2 * k + ck) << 4) ^ sw));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(s[m][nt], f[0], f[1], f[2], f[3], q[k][nt][0], q[k][nt][1]);
-                    }
+                scores([&](uint32_t (&f)[4], int k, int m) { ldsm_x4(f, at + m * (32 * D) + (((2 * k + ck) << 4) ^ sw)); });
             } else {
                 // lane's row address of the four 8 x 8 blocks: channels + 8 (lane / 16), token chunk (lane / 8) % 2
                 const int r = lane & 7, chb = r + ((lane >> 4) << 3), ck = (lane >> 3) & 1;
                 const uint32_t at = smem_addr(hat) + chb * 64, sw = ((chb >> 1) & 3) << 4;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t f[4];
-                        ldsm_x4_t(f, at + k * 1024 + ((((2 * m + ck) << 4)) ^ sw));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(s[m][nt], f[0], f[1], f[2], f[3], q[k][nt][0], q[k][nt][1]);
-                    }
+                scores([&](uint32_t (&f)[4], int k, int m) { ldsm_x4_t(f, at + k * 1024 + ((((2 * m + ck) << 4)) ^ sw)); });
             }
             // logits in log2 units; -inf where the row does not attend the token
 #pragma unroll
