@@ -369,8 +369,9 @@ static __device__ __noinline__ void att_locate(const kivi_cache* c, const Attend
         range[1] = p;
 }
 
-// What the workers need of a tile, written by the copy warp.
-struct AttDesc {
+// What the workers need of a tile, written by the copy warp.  Aligned, so
+// that its fields may be read several at a time (128 rows: 300 against 302 us).
+struct alignas(16) AttDesc {
     int b, rr;
     int nuq;                  // 32-token units of quantized tokens, 0 .. 4
     int f0;                   // fp16 token (residual, then drafts) at position 0 of the tile; negative before them
