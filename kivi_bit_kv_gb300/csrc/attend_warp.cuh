@@ -33,8 +33,8 @@
 // copies have landed (a bounded wait as well).
 //
 // Measured: one row a KV head over 1024 listed tokens and the residual of 64
-// ragged int2 sequences of 32 heads (418 MB): 162 us, 2.6 TB/s; 8 rows over a
-// 2065-token int4 prefix of 32 x 32 heads (420 MB): 169 us, 2.5 TB/s; 16 rows
+// ragged int2 sequences of 32 heads (418 MB): 161 us, 2.6 TB/s; 8 rows over a
+// 2065-token int4 prefix of 32 x 32 heads (420 MB): 170 us, 2.5 TB/s; 16 rows
 // over eight int2 sequences of 4096 tokens (152 MB): 124 us.  Chains of
 // dependent instructions bound it: some 1200 instructions a unit of 4096
 // elements of K and of V each, issued in 52 % of the cycles by the four warps
@@ -493,47 +493,47 @@ attend_warp_kernel(const __grid_constant__ kivi_cache c, const __grid_constant__
 
             // S^T: tokens 16 m + g (+ 8), rows 8 nt + 2 tq (+ 1).  The tensor core
             // truncates its sums: a chain of n steps of 16 channels loses some (n + 1) / 2
-            // units of 2^-23 of its sum, 8.5 with all of D = 256 in one, 2.5 in chains
-            // of 64 channels that are added with rounding (the same time: 197 and 203 us
-            // for 1 and 8 rows of B 8, H 32, T 4096).  D = 128 keeps one chain, 4.5
-            // units: two cost 1 % there.
+            // units of 2^-23 of its sum.  Chains of 64 channels side by side, added
+            // with rounding, lose 2.5 at every D; one chain through all channels loses
+            // 8.5 at D = 256, where it is also slower (203 against 200 us, 8 rows of B 8,
+            // H 32, T 4096), and 4.5 at D = 128 (169.6 against 170.8 us, 8 int4 rows).
             float s[2][NT][4];
             auto scores = [&](auto&& load) {
-                constexpr int KC = D == 256 ? 4 : D / 16;
+                constexpr int KC = 4, NC = D / 16 / KC;  // steps of a chain, chains
+                float y[NC][2][NT][4];
 #pragma unroll
-                for (int k0 = 0; k0 < D / 16; k0 += KC) {
-                    float y[2][NT][4];
+                for (int x = 0; x < NC; ++x)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                y[m][nt][k] = 0.0f;
+                                y[x][m][nt][k] = 0.0f;
 #pragma unroll
-                    for (int k = k0; k < k0 + KC; ++k)
+                for (int k = 0; k < KC; ++k)
+#pragma unroll
+                    for (int x = 0; x < NC; ++x)
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             uint32_t f[4];
-                            load(f, k, m);
+                            load(f, k + x * KC, m);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(y[m][nt], f[0], f[1], f[2], f[3], q[k][nt][0], q[k][nt][1]);
+                                mma_f16(y[x][m][nt], f[0], f[1], f[2], f[3], q[k + x * KC][nt][0], q[k + x * KC][nt][1]);
                         }
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int k = 0; k < 4; k += 2) {
-                                if (k0 == 0) {
-                                    s[m][nt][k] = y[m][nt][k];
-                                    s[m][nt][k + 1] = y[m][nt][k + 1];
-                                } else {
-                                    add_pair(s[m][nt] + k, y[m][nt] + k);
-                                }
-                            }
-                }
+                        for (int k = 0; k < 4; k += 2) {
+#pragma unroll
+                            for (int x = 1; x < NC; ++x)
+                                add_pair(y[0][m][nt] + k, y[x][m][nt] + k);
+                            s[m][nt][k] = y[0][m][nt][k];
+                            s[m][nt][k + 1] = y[0][m][nt][k + 1];
+                        }
             };
             if (__builtin_expect(!go, 0)) {
                 // fp16 keys: blocks token + 8 (lane / 8) % 2, channel chunk lane / 16
