@@ -401,6 +401,131 @@ int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k,
                          int32_t P, const int32_t* counts, int32_t* status,
                          void* stream);
 
+/* --------------------------------------- the ends of a speculative step ---- */
+
+/*
+ * What stands before and after kivi_tree_attention and kivi_append_path in a
+ * decode loop: queries, keys and values out of a layer's projections, and
+ * the accepted path out of the model's logits.  The pages have no counterpart.
+ * None of these calls needs a workspace, each is one kernel on `stream`, and the
+ * same inputs give the same bits.  Outputs must not overlap inputs.
+ */
+
+/* Types of an input tensor. */
+#define KIVI_F16  0 /* IEEE binary16 */
+#define KIVI_BF16 1
+#define KIVI_F32  2
+
+/* Largest number of position axes of one kivi_norm_rope call. */
+#define KIVI_MAX_AXES 8
+
+/*
+ * Arguments of kivi_norm_rope: N tokens per sequence.  Inputs have the
+ * channels of a head side by side; strides of sequences, tokens and heads are
+ * in elements, so that views into one projection's output serve as well as
+ * tensors of their own.  Strides (of dimensions larger than one) and
+ * pointers are multiples of 16 bytes.  An input and its output may both
+ * be NULL: that group of heads is left out (not all three).
+ */
+typedef struct kivi_heads {
+    int32_t Hq, N;
+    int32_t dtype;          /* of q_in, k_in and v_in: KIVI_F16, KIVI_BF16 or KIVI_F32 */
+    int32_t rot;            /* rotated channels of a head: a multiple of 16, 0 .. D   */
+    int32_t interleaved;    /* 0: channel j pairs with j + rot/2; 1: 2j with 2j + 1   */
+    int32_t n_axes;         /* position axes, 1 .. KIVI_MAX_AXES                       */
+    float eps;              /* added to the mean of squares, >= 0                      */
+    int32_t reserved;       /* 0 */
+    const void *q_in, *k_in, *v_in;                     /* [B][N][Hq, H, H][D]        */
+    int64_t q_strides[3], k_strides[3], v_strides[3];   /* sequence, token, head      */
+    const float* q_weight;  /* fp32 [D] or NULL: queries are not normalized            */
+    const float* k_weight;  /* the same of the keys                                    */
+    const float* inv_freq;  /* fp32 [rot/2]: angle of a pair per position (rot > 0)    */
+    const int32_t* axis;    /* int32 [rot/2]: axis of a pair, or NULL: axis 0          */
+    const int32_t* pos;     /* int32 [n_axes][B][N], or NULL: token i is at i          */
+    const int32_t* base;    /* int32 [B] added to every position, or NULL              */
+    const int32_t* n_tok;   /* int32 [B], or NULL: N tokens everywhere                 */
+    uint16_t *q, *k, *v;    /* fp16 [B][Hq, H, H][N][D]                                */
+} kivi_heads;
+
+/*
+ * Queries, keys and values as the other entry points take them, in one pass over
+ * the projections: with x a head's D channels of a token,
+ *   y_d = x_d w_d / sqrt(mean_d x_d^2 + eps)     (q with q_weight, k with k_weight;
+ *                                                 y = x without a weight)
+ *   (y_a, y_c) -> (y_a cos t - y_c sin t, y_c cos t + y_a sin t)
+ * for the rot/2 pairs (a, c) of its first rot channels, t = position * inv_freq_j
+ * of pair j, position = (pos ? pos[axis_j][b][i] : i) + (base ? base[b] : 0) -- an
+ * int32 sum; with base = len the tokens follow the cached ones, with pos a token's
+ * depth in a draft tree, with several axes its frame, row and column.  An axis
+ * outside [0, n_axes) is taken as the nearest in it.  Values are converted only.
+ * The arithmetic is fp32 with the angle reduced in two terms (any int32 position;
+ * the error of an angle stays near 2^-24 for products t below 2^24), rounded to fp16
+ * once.  Sums of squares are fp32: a row whose sum exceeds its range gives 0.
+ * n_tok[b] is taken as min(n_tok[b], N) (0 if negative): tokens from there on are
+ * not read and their rows left as they were.  Only B, H and D of the descriptor
+ * are read, and its memory's device is checked.
+ */
+int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream);
+
+/* Largest vocabulary of kivi_token_probs and kivi_verify_tree. */
+#define KIVI_MAX_VOCAB (1 << 20)
+
+/*
+ * Probabilities of N rows of logits per sequence:
+ *   probs[b][i][x] = exp((l_x - max_y l_y) / T_b) / sum_z exp((l_z - max_y l_y) / T_b)
+ * with T = temperature (fp32 [B], or NULL: 1 everywhere).  T_b <= 0 puts all on the
+ * largest logit, the first among equal ones.  logits: B x N rows of V values of
+ * type dtype, strides of sequences and rows in elements (any: a padded vocabulary,
+ * rows that start at odd elements); probs: fp32 [B][N][V]; 1 <= V <=
+ * KIVI_MAX_VOCAB.  n_rows (int32 [B], or NULL: N everywhere) is taken as
+ * min(n_rows[b], N) (0 if negative): rows from there on are neither read nor
+ * written.  fp32 arithmetic.  A row of -infinity alone is 0; a row with a NaN or
+ * +infinity, or whose T_b is NaN, is NaN.
+ */
+int32_t kivi_token_probs(const void* logits, int32_t dtype, int32_t B,
+                         int32_t N, int32_t V, int64_t batch_stride,
+                         int64_t row_stride, const float* temperature,
+                         const int32_t* n_rows, float* probs, void* stream);
+
+/*
+ * Verification of a draft against the target's probabilities, from given
+ * uniform random numbers.  Node 0 of a sequence's tree is its pending token
+ * (sampled, not yet in the cache), nodes i >= 1 are drafted tokens; node i's
+ * parent has a lower index.  target[b][i]: the model's probabilities of the token
+ * after node i.  draft[b][i]: those from which node i's children were drawn
+ * independently, or NULL if drafts were not drawn (the best tokens, say).
+ * From node 0, the children of the current node c are tested in ascending order
+ * with rho = target[b][c], s = 1 at first:
+ *   accept i if  u_i draft[c][x] < rho_x s      (x = tokens[i]; NULL: u_i < rho_x s)
+ *   otherwise    rho = max(rho s - draft[c], 0) (NULL: rho_x = 0),
+ *                s = 2^42 / Z,  Z = sum_y w(rho_y)       (s = 0 for Z = 0)
+ * and an accepted child becomes the current node.  When no child is left, the
+ * next token is the first x at which the running sum of w(rho) exceeds
+ * floor(Z floor(2^32 u_0) / 2^32); with Z = 0, rho is target[b][c] again.  So the
+ * tokens follow the target's distribution whatever the draft was.  The
+ * arithmetic is exact where order could matter, and results are the same on any
+ * implementation: probabilities are clamped to [0, 1] (NaN to 0), w(r) = r 2^42
+ * rounded to an int64 (half to even), products and differences are fp32, each
+ * rounded, s is the fp32 rounding of the fp64 quotient, and u_0 is clamped to
+ * [0, 1 - 2^-32] (NaN to 0).
+ *   path[b][0 .. counts[b]) = the kept nodes, 0 first, then -1: the path and
+ * counts of kivi_append_path (P = N).  next[b] = the next pending token, -1 if
+ * the last node's row of target is all zero.
+ * tokens, parent: int32 [B][N]; u: fp32 [B][N]; target, draft: fp32 [B][N][V];
+ * path: int32 [B][N]; counts, next: int32 [B]; 1 <= N <= KIVI_MAX_DRAFT, 1 <= V <=
+ * KIVI_MAX_VOCAB.  n_draft (int32 [B], or NULL: N everywhere) gives the nodes of
+ * each sequence, taken as min(n_draft[b], N); without any (0 or less) counts[b] =
+ * 0 and next[b] = -1.  parent[b][0] and tokens[b][0] are not read.  A node whose
+ * parent is not of lower index, or whose token is outside [0, V), is never
+ * accepted and changes nothing.
+ */
+int32_t kivi_verify_tree(int32_t B, int32_t N, int32_t V,
+                         const int32_t* tokens, const int32_t* parent,
+                         const int32_t* n_draft, const float* u,
+                         const float* target, const float* draft,
+                         int32_t* path, int32_t* counts, int32_t* next,
+                         void* stream);
+
 /* ------------------------------------------------ compact payload (store) */
 
 /*
@@ -477,8 +602,8 @@ int32_t kivi_import(const kivi_cache* c, const void* src, size_t src_bytes,
 /*
  * A library built with KIVI_CHECKS defined (the "checked" build variant)
  * checks, on the device, every global access of the encode, materialize,
- * append, payload, split-decode, selection and sparse and tree attention
- * kernels against the arrays of the cache and the buffers of the call (its
+ * append, payload, split-decode, selection, sparse and tree attention,
+ * head, probability and verification kernels against the arrays of the cache and the buffers of the call (its
  * workspace among them), and skips an access that falls outside them;
  * the streamed fused decode checks its copies, tiles and output rows and
  * reports in its workspace status word (kivi_decode_attention).  This call

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -37,7 +38,8 @@ EXPORTS = (
     "kivi_workspace_bytes", "kivi_decode_pv_noalloc", "kivi_decode_attention",
     "kivi_codec_fingerprint", "kivi_payload_bytes", "kivi_export", "kivi_import",
     "kivi_check_status", "kivi_block_select", "kivi_sparse_attention", "kivi_tree_attention",
-    "kivi_attend_workspace_bytes", "kivi_append_path",
+    "kivi_attend_workspace_bytes", "kivi_append_path", "kivi_norm_rope", "kivi_token_probs",
+    "kivi_verify_tree",
 )
 
 KIVI_PAYLOAD_MAGIC = 0x5056494B
@@ -47,6 +49,11 @@ KIVI_PAYLOAD_HEADER_BYTES = 64
 KIVI_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 KIVI_MAX_DRAFT = 256
+KIVI_MAX_AXES = 8
+KIVI_MAX_VOCAB = 1 << 20
+
+KIVI_F16, KIVI_BF16, KIVI_F32 = range(3)
+_DTYPES = {torch.float16: KIVI_F16, torch.bfloat16: KIVI_BF16, torch.float32: KIVI_F32}
 
 
 class KiviError(RuntimeError):
@@ -65,6 +72,11 @@ class kivi_cache(C.Structure):
         ("vq", C.c_void_p), ("vscale", C.c_void_p), ("vzero", C.c_void_p),
         ("kres", C.c_void_p), ("vres", C.c_void_p), ("len", C.c_void_p),
     ]
+
+
+# The C struct kivi_heads: Hq, N, dtype, rot, interleaved, n_axes, eps, reserved; the
+# inputs; nine strides; q_weight, k_weight, inv_freq, axis, pos, base, n_tok; the outputs.
+_HEADS = struct.Struct("=6ifi3Q9q7Q3Q")
 
 
 _LIB = None
@@ -108,6 +120,9 @@ def load(path: str | None = None):
         "kivi_tree_attention": ([cp, vp, i32, i32, vp, vp, vp, vp, f32, vp, vp, sz, vp], i32),
         "kivi_attend_workspace_bytes": ([cp, i32, i32], sz),
         "kivi_append_path": ([cp, vp, vp, i32, vp, i32, vp, vp, vp], i32),
+        "kivi_norm_rope": ([cp, vp, vp], i32),
+        "kivi_token_probs": ([vp, i32, i32, i32, i32, C.c_int64, C.c_int64, vp, vp, vp, vp], i32),
+        "kivi_verify_tree": ([i32, i32, i32] + [vp] * 10, i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -426,6 +441,147 @@ def kivi_append_path(cache, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor
     _call(load().kivi_append_path, "kivi_append_path", dev, C.byref(cache.desc), _ptr(k, torch.float16, "k", dev),
           _ptr(v, torch.float16, "v", dev), N, _ptr(path, torch.int32, "path", dev), P,
           _ptr(counts, torch.int32, "counts", dev), _ptr(status, torch.int32, "status", dev),
+          _raw_stream(stream, dev))
+
+
+def _rows_ptr(t: torch.Tensor, dtype, name: str, device) -> int:
+    """Pointer of an input whose last dimension is contiguous (any other strides)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def kivi_norm_rope(cache, q_in: torch.Tensor | None, k_in: torch.Tensor | None, v_in: torch.Tensor | None,
+                   q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
+                   inv_freq: torch.Tensor | None, pos: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                   axis: torch.Tensor | None = None, interleaved: bool = False, q_weight: torch.Tensor | None = None,
+                   k_weight: torch.Tensor | None = None, eps: float = 1e-6, n_tok: torch.Tensor | None = None,
+                   stream=None):
+    """q fp16 [B, Hq, N, D], k, v fp16 [B, H, N, D] <- the projections q_in
+    [B, N, Hq, D], k_in, v_in [B, N, H, D] (fp16, bf16 or fp32; any strides of 16
+    bytes but contiguous channels, so views of one fused projection will do):
+    heads of q and k with a weight fp32 [D] are RMS-normalized, then the first
+    2 len(inv_freq) channels rotated by position * inv_freq (fp32 [rot/2]; None
+    rotates nothing).  Positions: pos int32 [B, N] or [n_axes, B, N] (None: the
+    token's index) plus base int32 [B]; axis int32 [rot/2] picks a pair's axis.
+    interleaved pairs channels 2j and 2j + 1 instead of j and j + rot/2.  n_tok
+    int32 [B]: tokens of each sequence (rows from there on keep their
+    contents).  An input and its output may both be None."""
+    B, H, D, dev = cache.B, cache.H, cache.D, cache.device
+    first = q_in if q_in is not None else k_in if k_in is not None else v_in
+    if first is None:
+        raise ValueError("q_in, k_in and v_in are all None")
+    if first.dim() != 4:
+        _bad_shape(first, "q_in, k_in, v_in", (B, "N", "heads", D))
+    N, dtype = first.shape[1], first.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"projections must be fp16, bf16 or fp32, got {dtype}")
+    Hq = q_in.shape[2] if q_in is not None and q_in.dim() == 4 else H
+    ptrs, strides, outs = [], [], []
+    for name, x, y, heads in (("q", q_in, q, Hq), ("k", k_in, k, H), ("v", v_in, v, H)):
+        if x is None or y is None:
+            if x is not y:
+                raise ValueError(f"{name}_in and {name} are given together or not at all")
+            ptrs.append(0)
+            strides += (0, 0, 0)
+            outs.append(0)
+            continue
+        if x.shape != (B, N, heads, D):
+            _bad_shape(x, name + "_in", (B, N, heads, D))
+        if y.shape != (B, heads, N, D):
+            _bad_shape(y, name, (B, heads, N, D))
+        st = x.stride()
+        if st[3] != 1:
+            raise ValueError(f"{name}_in must have contiguous channels")
+        ptrs.append(_rows_ptr(x, dtype, name + "_in", dev))
+        strides += st[:3]
+        outs.append(_ptr(y, torch.float16, name, dev))
+    half = 0 if inv_freq is None else inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    if half < 0:
+        _bad_shape(inv_freq, "inv_freq", ("rot/2",))
+    n_axes = 1
+    if pos is not None:
+        n_axes = pos.shape[0] if pos.dim() == 3 else 1
+        if pos.shape != (B, N) and pos.shape != (n_axes, B, N):
+            _bad_shape(pos, "pos", (B, N), ("n_axes", B, N))
+    if axis is not None and axis.shape != (half,):
+        _bad_shape(axis, "axis", (half,))
+    for name, t, n in (("base", base, B), ("n_tok", n_tok, B), ("q_weight", q_weight, D), ("k_weight", k_weight, D)):
+        if t is not None and t.shape != (n,):
+            _bad_shape(t, name, (n,))
+    args = _HEADS.pack(
+        Hq, N, _DTYPES[dtype], 2 * half, int(bool(interleaved)), n_axes, eps, 0, *ptrs, *strides,
+        0 if q_weight is None else _ptr(q_weight, torch.float32, "q_weight", dev),
+        0 if k_weight is None else _ptr(k_weight, torch.float32, "k_weight", dev),
+        _ptr(inv_freq, torch.float32, "inv_freq", dev) if half else 0,
+        0 if axis is None or not half else _ptr(axis, torch.int32, "axis", dev),
+        0 if pos is None else _ptr(pos, torch.int32, "pos", dev),
+        0 if base is None else _ptr(base, torch.int32, "base", dev),
+        0 if n_tok is None else _ptr(n_tok, torch.int32, "n_tok", dev), *outs)
+    _call(load().kivi_norm_rope, "kivi_norm_rope", dev, C.byref(cache.desc), args, _raw_stream(stream, dev))
+
+
+def kivi_token_probs(logits: torch.Tensor, probs: torch.Tensor, temperature: torch.Tensor | None = None,
+                     n_rows: torch.Tensor | None = None, stream=None):
+    """probs fp32 [B, N, V] <- softmax of logits [B, N, V] (fp16, bf16 or fp32;
+    contiguous rows, any other strides) over temperature fp32 [B] (None: 1; 0: all
+    on the first of the largest).  n_rows int32 [B]: rows of each sequence (rows from
+    there on are left as they were)."""
+    if logits.dim() != 3:
+        _bad_shape(logits, "logits", ("B", "N", "V"))
+    B, N, V = logits.shape
+    dev = probs.device
+    if probs.shape != (B, N, V):
+        _bad_shape(probs, "probs", (B, N, V))
+    if temperature is not None and temperature.shape != (B,):
+        _bad_shape(temperature, "temperature", (B,))
+    if n_rows is not None and n_rows.shape != (B,):
+        _bad_shape(n_rows, "n_rows", (B,))
+    dtype = logits.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"logits must be fp16, bf16 or fp32, got {dtype}")
+    sb, sn, sv = logits.stride()
+    if sv != 1 and V > 1:
+        raise ValueError("logits must have contiguous rows")
+    pp = _ptr(probs, torch.float32, "probs", dev)
+    _call(load().kivi_token_probs, "kivi_token_probs", dev, _rows_ptr(logits, dtype, "logits", dev), _DTYPES[dtype],
+          B, N, V, sb, sn, None if temperature is None else _ptr(temperature, torch.float32, "temperature", dev),
+          None if n_rows is None else _ptr(n_rows, torch.int32, "n_rows", dev), pp, _raw_stream(stream, dev))
+
+
+def kivi_verify_tree(tokens: torch.Tensor, parent: torch.Tensor, u: torch.Tensor, target: torch.Tensor,
+                     draft: torch.Tensor | None, path: torch.Tensor, counts: torch.Tensor, next: torch.Tensor,
+                     n_draft: torch.Tensor | None = None, stream=None):
+    """path int32 [B, N], counts int32 [B] (as kivi_append_path takes them) and next
+    int32 [B] <- the accepted nodes of each tree and the token after them, from the
+    target's probabilities fp32 [B, N, V] after each node, the draft's fp32
+    [B, N, V] from which a node's children were drawn (None: not drawn), tokens,
+    parent int32 [B, N] (node 0: the pending token; parents have lower indices) and
+    uniform numbers u fp32 [B, N] (u[:, 0] draws the next token).  n_draft int32
+    [B]: nodes of each tree."""
+    if target.dim() != 3:
+        _bad_shape(target, "target", ("B", "N", "V"))
+    B, N, V = target.shape
+    dev = target.device
+    for name, t in (("tokens", tokens), ("parent", parent), ("u", u), ("path", path)):
+        if t.shape != (B, N):
+            _bad_shape(t, name, (B, N))
+    for name, t in (("counts", counts), ("next", next), ("n_draft", n_draft)):
+        if t is not None and t.shape != (B,):
+            _bad_shape(t, name, (B,))
+    if draft is not None and draft.shape != (B, N, V):
+        _bad_shape(draft, "draft", (B, N, V))
+    i32, tp = torch.int32, _ptr(target, torch.float32, "target", dev)
+    _call(load().kivi_verify_tree, "kivi_verify_tree", dev, B, N, V, _ptr(tokens, i32, "tokens", dev),
+          _ptr(parent, i32, "parent", dev), None if n_draft is None else _ptr(n_draft, i32, "n_draft", dev),
+          _ptr(u, torch.float32, "u", dev), tp, None if draft is None else _ptr(draft, torch.float32, "draft", dev),
+          _ptr(path, i32, "path", dev), _ptr(counts, i32, "counts", dev), _ptr(next, i32, "next", dev),
           _raw_stream(stream, dev))
 
 

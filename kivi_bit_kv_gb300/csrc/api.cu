@@ -335,20 +335,25 @@ int32_t kivi_decode_attention(const kivi_cache* c, const uint16_t* q, int32_t Hq
 
 // ----------------------------------------- speculative and sparse decode ---
 
-// The kernels run on the current device: refuse a cache that lives on another.
-static int32_t check_current_device(const kivi_cache* c)
+// The kernels run on the current device: refuse memory that lives on another.
+static int32_t check_on_device(const void* p, const char* what, const char* buffer)
 {
     cudaPointerAttributes a;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, c->kq) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
         (void)cudaGetLastError();
-        return fail(KIVI_ECUDA, "the current device or the cache's memory could not be queried");
+        return fail(KIVI_ECUDA, "the current device or %s's memory could not be queried", what);
     }
     if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
-        return fail(KIVI_EINVAL, "cache buffer kq is not device memory");
+        return fail(KIVI_EINVAL, "%s is not device memory", buffer);
     if (a.type == cudaMemoryTypeDevice && a.device != dev)
-        return fail(KIVI_EINVAL, "the cache is on device %d, the current device is %d", a.device, dev);
+        return fail(KIVI_EINVAL, "%s is on device %d, the current device is %d", what, a.device, dev);
     return KIVI_OK;
+}
+
+static int32_t check_current_device(const kivi_cache* c)
+{
+    return check_on_device(c->kq, "the cache", "cache buffer kq");
 }
 
 static int32_t check_blocks(const kivi_cache* c, const int32_t* blocks, int32_t n_keep)
@@ -461,6 +466,148 @@ int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k, const uint16_t*
     return launched(kivi::launch_append_path(*c, k, v, N, path, P, counts, status, (cudaStream_t)stream));
 }
 
+// --------------------------------------- the ends of a speculative step ---
+
+static int32_t check_aligned4(const void* p, const char* name)  // NULL is fine
+{
+    return ((uintptr_t)p & 3u) ? fail(KIVI_EINVAL, "%s is not 4-byte aligned", name) : KIVI_OK;
+}
+
+static int32_t check_dtype(int32_t dtype)
+{
+    if (dtype != KIVI_F16 && dtype != KIVI_BF16 && dtype != KIVI_F32)
+        return fail(KIVI_EINVAL, "dtype=%d unsupported; valid: KIVI_F16 (0), KIVI_BF16 (1), KIVI_F32 (2)", dtype);
+    return KIVI_OK;
+}
+
+// One group of heads of kivi_norm_rope: its input, strides and output.
+static int32_t check_projection(const kivi_heads* a, const char* name, const void* in, const int64_t* strides,
+                                const uint16_t* out, int32_t B, int32_t heads, const float* weight)
+{
+    if (!in && !out)
+        return KIVI_OK;
+    if (!in || !out)
+        return fail(KIVI_EINVAL, "%s: an input and its output are given together or not at all", name);
+    if (!aligned16(in) || !aligned16(out))
+        return fail(KIVI_EINVAL, "%s: the input or the output is not 16-byte aligned", name);
+    const int32_t dims[3] = {B, a->N, heads};
+    const int64_t unit = a->dtype == KIVI_F32 ? 4 : 8;  // elements of 16 bytes
+    for (int i = 0; i < 3; ++i)
+        if (dims[i] > 1 && strides[i] % unit != 0)
+            return fail(KIVI_EINVAL, "%s: stride %lld of dimension %d is not a multiple of 16 bytes", name,
+                        (long long)strides[i], i);
+    if (weight && !aligned16(weight))
+        return fail(KIVI_EINVAL, "%s_weight is not 16-byte aligned", name);
+    return KIVI_OK;
+}
+
+int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream)
+{
+    NvtxRange range_("kivi_norm_rope");
+    int32_t st = check_cache(c);
+    if (st != KIVI_OK)
+        return st;
+    if (!a)
+        return fail(KIVI_EINVAL, "kivi_heads is NULL");
+    if ((st = check_heads(c, a->Hq)) != KIVI_OK || (st = check_dtype(a->dtype)) != KIVI_OK)
+        return st;
+    if (a->N < 1 || (long long)c->B * a->N >= (1ll << 27))
+        return fail(KIVI_EINVAL, "N=%d: must be >= 1 with B*N < 2^27 tokens", a->N);
+    if (a->rot < 0 || a->rot > c->D || a->rot % 16 != 0)
+        return fail(KIVI_EINVAL, "rot=%d must be a multiple of 16 in [0, D=%d]", a->rot, c->D);
+    if (a->n_axes < 1 || a->n_axes > KIVI_MAX_AXES)
+        return fail(KIVI_EINVAL, "n_axes=%d; valid: 1 .. %d", a->n_axes, KIVI_MAX_AXES);
+    if (!(a->eps >= 0.0f) || a->eps > 3.402823466e38f)
+        return fail(KIVI_EINVAL, "eps must be finite and >= 0");
+    if (!a->q_in && !a->k_in && !a->v_in)
+        return fail(KIVI_EINVAL, "q_in, k_in and v_in are all NULL");
+    if ((st = check_projection(a, "q", a->q_in, a->q_strides, a->q, c->B, a->Hq, a->q_weight)) != KIVI_OK ||
+        (st = check_projection(a, "k", a->k_in, a->k_strides, a->k, c->B, c->H, a->k_weight)) != KIVI_OK ||
+        (st = check_projection(a, "v", a->v_in, a->v_strides, a->v, c->B, c->H, nullptr)) != KIVI_OK)
+        return st;
+    if (a->rot > 0 && (st = check_ptr(a->inv_freq, "inv_freq", false)) != KIVI_OK)
+        return st;
+    if ((st = check_aligned4(a->axis, "axis")) != KIVI_OK || (st = check_aligned4(a->pos, "pos")) != KIVI_OK ||
+        (st = check_aligned4(a->base, "base")) != KIVI_OK || (st = check_aligned4(a->n_tok, "n_tok")) != KIVI_OK ||
+        (st = check_current_device(c)) != KIVI_OK)
+        return st;
+    return launched(kivi::launch_norm_rope(*c, *a, (cudaStream_t)stream));
+}
+
+// B sequences of N rows over V tokens.
+static int32_t check_vocab(int32_t B, int32_t N, int32_t V)
+{
+    if (B < 1 || N < 1 || (long long)B * N >= (1ll << 27))
+        return fail(KIVI_EINVAL, "B=%d N=%d: both must be >= 1 with B*N < 2^27", B, N);
+    if (V < 1 || V > KIVI_MAX_VOCAB)
+        return fail(KIVI_EINVAL, "vocabulary V=%d; valid: 1 .. %d", V, KIVI_MAX_VOCAB);
+    return KIVI_OK;
+}
+
+int32_t kivi_token_probs(const void* logits, int32_t dtype, int32_t B, int32_t N, int32_t V, int64_t batch_stride,
+                         int64_t row_stride, const float* temperature, const int32_t* n_rows, float* probs,
+                         void* stream)
+{
+    NvtxRange range_("kivi_token_probs");
+    int32_t st;
+    if ((st = check_dtype(dtype)) != KIVI_OK || (st = check_vocab(B, N, V)) != KIVI_OK ||
+        (st = check_ptr(probs, "probs")) != KIVI_OK)
+        return st;
+    if (!logits)
+        return fail(KIVI_EINVAL, "logits is NULL");
+    if ((uintptr_t)logits & (dtype == KIVI_F32 ? 3u : 1u))
+        return fail(KIVI_EINVAL, "logits is not aligned to its elements");
+    if ((st = check_aligned4(temperature, "temperature")) != KIVI_OK ||
+        (st = check_aligned4(n_rows, "n_rows")) != KIVI_OK ||
+        (st = check_on_device(probs, "probs", "probs")) != KIVI_OK)
+        return st;
+    kivi::ProbsArgs a = {};
+    a.logits = logits;
+    a.dtype = dtype;
+    a.B = B;
+    a.N = N;
+    a.V = V;
+    a.batch_stride = batch_stride;
+    a.row_stride = row_stride;
+    a.temperature = temperature;
+    a.n_rows = n_rows;
+    a.probs = probs;
+    return launched(kivi::launch_token_probs(a, (cudaStream_t)stream));
+}
+
+int32_t kivi_verify_tree(int32_t B, int32_t N, int32_t V, const int32_t* tokens, const int32_t* parent,
+                         const int32_t* n_draft, const float* u, const float* target, const float* draft,
+                         int32_t* path, int32_t* counts, int32_t* next, void* stream)
+{
+    NvtxRange range_("kivi_verify_tree");
+    int32_t st = check_vocab(B, N, V);
+    if (st != KIVI_OK)
+        return st;
+    if (N > KIVI_MAX_DRAFT)
+        return fail(KIVI_EINVAL, "N=%d nodes; valid: 1 .. %d", N, KIVI_MAX_DRAFT);
+    if ((st = check_ptr(tokens, "tokens", false)) != KIVI_OK || (st = check_ptr(parent, "parent", false)) != KIVI_OK ||
+        (st = check_aligned4(n_draft, "n_draft")) != KIVI_OK || (st = check_ptr(u, "u", false)) != KIVI_OK ||
+        (st = check_ptr(target, "target")) != KIVI_OK || (draft && (st = check_ptr(draft, "draft")) != KIVI_OK) ||
+        (st = check_ptr(path, "path", false)) != KIVI_OK || (st = check_ptr(counts, "counts", false)) != KIVI_OK ||
+        (st = check_ptr(next, "next", false)) != KIVI_OK ||
+        (st = check_on_device(target, "target", "target")) != KIVI_OK)
+        return st;
+    kivi::VerifyArgs a = {};
+    a.tokens = tokens;
+    a.parent = parent;
+    a.n_draft = n_draft;
+    a.u = u;
+    a.target = target;
+    a.draft = draft;
+    a.path = path;
+    a.counts = counts;
+    a.next = next;
+    a.B = B;
+    a.N = N;
+    a.V = V;
+    return launched(kivi::launch_verify_tree(a, (cudaStream_t)stream));
+}
+
 // ------------------------------------------------------ compact payload ---
 
 uint64_t kivi_codec_fingerprint(const kivi_cache* c)
@@ -546,7 +693,9 @@ int32_t kivi_check_status(int32_t* status)
                              kivi::check_word_append(),   kivi::check_word_payload(),
                              kivi::check_word_decode(),   kivi::check_word_decode_d64(),
                              kivi::check_word_decode_d128(), kivi::check_word_decode_d256(),
-                             kivi::check_word_select(),   kivi::check_word_attend()};
+                             kivi::check_word_select(),   kivi::check_word_attend(),
+                             kivi::check_word_rope(),     kivi::check_word_probs(),
+                             kivi::check_word_verify()};
     for (const int32_t w : words) {
         if (w == KIVI_ECUDA)
             return fail(KIVI_ECUDA, "reading the device check words failed");

@@ -71,6 +71,18 @@ static inline cudaError_t set_check_ranges(const kivi_cache& c, cudaStream_t s,
         }
     return cudaMemcpyToSymbolAsync(g_check_ranges, r, sizeof r, 0, cudaMemcpyHostToDevice, s);
 }
+// The same for a call without a cache.
+static inline cudaError_t set_check_buffers(cudaStream_t s, std::initializer_list<CallBuf> call)
+{
+    CheckRange r[kCheckRanges] = {};
+    int n = 0;
+    for (const CallBuf& b : call)
+        if (b.p && n < kCheckRanges) {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(b.p);
+            r[n++] = CheckRange{lo, lo + b.bytes};
+        }
+    return cudaMemcpyToSymbolAsync(g_check_ranges, r, sizeof r, 0, cudaMemcpyHostToDevice, s);
+}
 // Reads and clears this translation unit's check word (synchronizes).
 static inline int32_t take_check_word()
 {
@@ -87,10 +99,19 @@ static inline int32_t take_check_word()
         if (e_ != cudaSuccess)                                                \
             return e_;                                                        \
     } while (0)
+#define KIVI_SET_CHECK_BUFFERS(s, ...)                                        \
+    do {                                                                      \
+        const cudaError_t e_ = ::kivi::set_check_buffers((s), __VA_ARGS__);   \
+        if (e_ != cudaSuccess)                                                \
+            return e_;                                                        \
+    } while (0)
 #else
 #define KIVI_IN_RANGE(p, n) true
 #define KIVI_SET_CHECK_RANGES(c, s, ...) \
     do {                                 \
+    } while (0)
+#define KIVI_SET_CHECK_BUFFERS(s, ...) \
+    do {                               \
     } while (0)
 #endif
 

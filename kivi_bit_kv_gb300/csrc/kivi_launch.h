@@ -69,6 +69,28 @@ cudaError_t launch_attend_b(const kivi_cache& c, const AttendArgs& a, float* ws,
 // Workspace bytes of a call with N drafted tokens, and of any with up to N.
 size_t attend_ws_bytes(const kivi_cache& c, int Hq, int N);
 size_t attend_ws_bytes_upto(const kivi_cache& c, int Hq, int N);
+// Head norms, rotary positions and the head-major layout (checked arguments).
+cudaError_t launch_norm_rope(const kivi_cache& c, const kivi_heads& a, cudaStream_t s);
+// Probabilities of B x N rows of V logits, batch and row strides in elements.
+struct ProbsArgs {
+    const void* logits;
+    int64_t batch_stride, row_stride;
+    const float* temperature;  // [B] or NULL
+    const int32_t* n_rows;     // [B] or NULL
+    float* probs;              // [B][N][V]
+    int32_t dtype, B, N, V;
+};
+cudaError_t launch_token_probs(const ProbsArgs& a, cudaStream_t s);
+// Verification of B trees of up to N nodes over V tokens (include/kivi.h).
+struct VerifyArgs {
+    const int32_t *tokens, *parent;  // [B][N]
+    const int32_t* n_draft;          // [B] or NULL
+    const float* u;                  // [B][N]
+    const float *target, *draft;     // [B][N][V], draft may be NULL
+    int32_t *path, *counts, *next;   // [B][N], [B], [B]
+    int32_t B, N, V;
+};
+cudaError_t launch_verify_tree(const VerifyArgs& a, cudaStream_t s);
 cudaError_t launch_decode_qk(const kivi_cache& c, const uint16_t* q, int Hq, float sm_scale,
                              float* logits, int ld_logits, cudaStream_t s);
 // ws_o: [B*Hq][nchunks][D], ws_m / ws_l: [B*Hq][nchunks] (fp32).
@@ -126,6 +148,9 @@ int32_t check_word_select();
 template <int D, int B>
 int32_t check_word_attend_b();
 int32_t check_word_attend();
+int32_t check_word_rope();
+int32_t check_word_probs();
+int32_t check_word_verify();
 #endif
 
 // Sets the message kivi_last_error() returns on this host thread; returns status.
