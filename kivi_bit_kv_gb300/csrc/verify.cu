@@ -23,8 +23,33 @@ typedef unsigned long long u64;
 
 __device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }  // NaN to 0
 
-// A probability as a multiple of 2^-42: sums of up to 2^20 of these are exact.
-__device__ __forceinline__ u64 whole(float r) { return (u64)__float2ll_rn(r * 0x1p42f); }
+// Probabilities as multiples of 2^-42, rounded half to even: sums of up to 2^20 of these
+// are exact.  The conversion to 64 bits is slow (it shares the fp64 pipe), so a value
+// below 4 is split in fp32: r + 4 rounds it to a = A 2^-21, r - a is exact and at most
+// 2^-22, and (r - a) 2^42 + 1.5 2^23 rounds that to a whole number B.  As A 2^21 is
+// even, A 2^21 + B is the rounded r 2^42.  The numbers add up as the bits of the
+// rounded sums; two of 32 bits hold those of some hundred values.
+struct Whole {
+    uint32_t a = 0, b = 0, n = 0;
+    __device__ __forceinline__ void add(float r)
+    {
+        const float t = __fadd_rn(r, 4.0f);
+        const float u = __fmaf_rn(__fsub_rn(r, __fsub_rn(t, 4.0f)), 0x1p42f, 0x1.8p23f);
+        a += __float_as_uint(t);
+        b += __float_as_uint(u);
+        ++n;  // a constant after unrolling
+    }
+    __device__ __forceinline__ u64 sum() const
+    {
+        return ((u64)(a - n * 0x40800000u) << 21) + (u64)(long long)(int)(b - n * 0x4b400000u);
+    }
+};
+__device__ __forceinline__ u64 whole(float r)
+{
+    Whole w;
+    w.add(r);
+    return w.sum();
+}
 
 __device__ __forceinline__ float scale_of(u64 z) { return z ? (float)__ddiv_rn(0x1p42, (double)z) : 0.0f; }
 
@@ -152,9 +177,12 @@ verify_tree_kernel(VerifyArgs a, int run)
     }
     cluster.barrier_wait(std::move(arrived));
     if (rank == 0)
-        for (int i = tid; i < (int)(sizeof(VerifyTree) / 4); i += kVerifyThreads)
+        for (int i = tid; i < 1 + 5 * N; i += kVerifyThreads) {  // n, then N words of each of the five arrays
+            const int at = i == 0 ? 0 : 1 + (i - 1) / N * KIVI_MAX_DRAFT + (i - 1) % N;
+            const int x = reinterpret_cast<const int*>(&sm.tree)[at];
             for (int r = 1; r < C; ++r)
-                reinterpret_cast<int*>(&cluster.map_shared_rank(&sm, r)->tree)[i] = reinterpret_cast<const int*>(&sm.tree)[i];
+                reinterpret_cast<int*>(&cluster.map_shared_rank(&sm, r)->tree)[at] = x;
+        }
     cluster.sync();
     const VerifyTree& t = sm.tree;
     const int g = rank * kVerifyWarps + warp;
@@ -169,11 +197,13 @@ verify_tree_kernel(VerifyArgs a, int run)
         for (int x = x0 + lane * W; x < x1; x += 32 * W * U) {
             float r[U][W];
             load_lines<W, U>(p, q, x, x1, sm.scale, k, r);
+            Whole w;
 #pragma unroll
             for (int i = 0; i < U; ++i)
 #pragma unroll
                 for (int j = 0; j < W; ++j)
-                    z += whole(r[i][j]);
+                    w.add(r[i][j]);
+            z += w.sum();
         }
         z = warp_sum(z);
         pass ^= 1;
@@ -195,6 +225,11 @@ verify_tree_kernel(VerifyArgs a, int run)
     int cur = 0, k = 0, count = t.n > 0 ? 1 : 0;
     u64 z = 0;
     for (int i = 1; (i = next_child(t, cur, i)) < t.n; ++i) {
+        if (k > 0) {  // s after a rejection, where a sibling is left to be tested
+            if (tid == 0)
+                sm.scale[k] = scale_of(z);
+            __syncthreads();
+        }
         float r = t.p[i];
         if (drawn)
             r = residual(r, t.q[i], sm.scale, k);
@@ -217,7 +252,6 @@ verify_tree_kernel(VerifyArgs a, int run)
         if (tid == 0) {
             sm.gone[k] = t.token[i];
             sm.gone_w[k] = whole(r);
-            sm.scale[k + 1] = scale_of(z);
         }
         __syncthreads();
         ++k;
@@ -264,14 +298,15 @@ verify_tree_kernel(VerifyArgs a, int run)
         u64 line[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            line[i] = 0;
+            Whole w;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 if (!drawn)
                     for (int m = 0; m < k; ++m)
                         r[i][j] = sm.gone[m] == x + i * 32 * W + j ? 0.0f : r[i][j];
-                line[i] += whole(r[i][j]);
+                w.add(r[i][j]);
             }
+            line[i] = w.sum();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
