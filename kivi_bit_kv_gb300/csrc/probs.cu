@@ -1,9 +1,9 @@
 // probs.cu -- probabilities of rows of logits, one temperature per sequence
 // (kivi_token_probs).
 //
-// A row is read once into the registers of a cluster of CTAs: each thread keeps a
-// running maximum and sum of its own values, the pairs are joined over warp, CTA and
-// cluster, and the quotients are written from the registers.
+// A row is read once, into the shared memory of a cluster of CTAs: each thread keeps a
+// running maximum and sum of its own values, the pairs are joined over the cluster, and
+// the quotients are formed from the values kept.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -20,8 +20,9 @@ namespace kivi {
 
 namespace cg = cooperative_groups;
 
-constexpr int kProbsThreads = 512, kProbsWarps = kProbsThreads / 32;
-constexpr int kProbsCluster = 8;  // most CTAs of a row
+constexpr int kProbsThreads = 256, kProbsWarps = kProbsThreads / 32, kProbsCtas = 5;
+constexpr int kProbsCluster = 8;    // most CTAs of a row
+constexpr int kProbsBytes = 32768;  // shared memory for a CTA's logits
 
 // log2(e) / T as hi + lo with lo > 0, so that a distance of -infinity gives
 // -infinity through both.  An infinite T gives equal weights to all finite logits, a
@@ -87,9 +88,12 @@ __device__ __forceinline__ F2 both(float a) { return pack2(a, a); }
 
 // Scale and reference of a row as the loops below use them, twice each.
 struct Scale2 {
-    F2 hi, lo, minus_ref;
+    F2 hi, lo, minus_ref, minus_hi, minus_lo;
 };
-__device__ __forceinline__ Scale2 twice(Scale c, float ref) { return {both(c.hi), both(c.lo), both(-ref)}; }
+__device__ __forceinline__ Scale2 twice(Scale c, float ref)
+{
+    return {both(c.hi), both(c.lo), both(-ref), both(-c.hi), both(-c.lo)};
+}
 
 // 2^(d (hi + lo)) of distances d = l - ref <= 0 from the largest logit; NaN for a NaN
 // d, 0 for -infinity.  For sums, whose terms' roundings cancel.
@@ -101,35 +105,43 @@ __device__ __forceinline__ F2 weights_sum(F2 l, const Scale2& c)
 }
 
 // The same times f, with the rounding of the exponent (half a unit of 2^-24 of up to
-// 126) made good: 2^(y + e) = 2^y (1 + e ln 2).  e is NaN or infinite only where 2^y
+// 126) made good: 2^(y + e) = 2^y (1 + e ln 2).  -e is NaN or infinite only where 2^y
 // is 0 or where the row's sum, and so f, is NaN.
 __device__ __forceinline__ F2 weights(F2 l, const Scale2& c, F2 f)
 {
-    const F2 d = add2(l, c.minus_ref);
-    const float2 y = unpack2(mul2(d, c.hi));
-    const float2 e = unpack2(fma2(d, c.lo, fma2(d, c.hi, pack2(-y.x, -y.y))));
-    const F2 w = mul2(pack2(exp2_ftz(y.x), exp2_ftz(y.y)), f);
-    return fma2(w, mul2(pack2(fminf(e.x, 1.0f), fminf(e.y, 1.0f)), both(0.693147181f)), w);
+    const F2 d = add2(l, c.minus_ref), y = mul2(d, c.hi);
+    const float2 e = unpack2(fma2(d, c.minus_lo, fma2(d, c.minus_hi, y)));
+    const F2 w = mul2(pack2(exp2_ftz(unpack2(y).x), exp2_ftz(unpack2(y).y)), f);
+    return fma2(w, mul2(pack2(fmaxf(e.x, -1.0f), fmaxf(e.y, -1.0f)), both(-0.693147181f)), w);
 }
 __device__ __forceinline__ float weight(float d, Scale c)
 {
     return unpack2(weights(both(d), twice(c, 0.0f), both(1.0f))).x;
 }
 
-// Four neighbouring logits as loaded: pair(i) in fp32.
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
+
+// Four neighbouring logits: pair(i) in fp32.
 template <class T>
 struct Raw4 {
     uint2 v;
-    __device__ __forceinline__ void load(const T* p)
-    {
-        if (KIVI_IN_RANGE(p, 8))
-            v = __ldg(reinterpret_cast<const uint2*>(p));
-    }
+    static constexpr int BYTES = 8;
     __device__ __forceinline__ void load_each(const T* p)
     {
         const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
         v.x = ldg_checked(q) | (uint32_t)ldg_checked(q + 1) << 16;
         v.y = ldg_checked(q + 2) | (uint32_t)ldg_checked(q + 3) << 16;
+    }
+    // From the two aligned vectors that hold them, `mis` logits into the first.
+    __device__ __forceinline__ void load_shifted(const T* p, int mis)
+    {
+        const uint2* q = reinterpret_cast<const uint2*>(p - mis);
+        const uint2 a = ldg_checked(q), b = ldg_checked(q + 1);
+        const unsigned long long lo = (unsigned long long)a.y << 32 | a.x, hi = (unsigned long long)b.y << 32 | b.x;
+        const unsigned long long w = lo >> (16 * mis) | hi << (64 - 16 * mis);
+        v = make_uint2((uint32_t)w, (uint32_t)(w >> 32));
     }
     __device__ __forceinline__ void clear()  // to -infinity
     {
@@ -148,19 +160,49 @@ struct Raw4 {
 template <>
 struct Raw4<float> {
     float4 v;
-    __device__ __forceinline__ void load(const float* p) { v = ld_nc_f4(p); }
+    static constexpr int BYTES = 16;
     __device__ __forceinline__ void load_each(const float* p)
     {
         v = make_float4(ldg_checked(p), ldg_checked(p + 1), ldg_checked(p + 2), ldg_checked(p + 3));
     }
+    __device__ __forceinline__ void load_shifted(const float* p, int) { load_each(p); }
     __device__ __forceinline__ void clear() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ float2 pair(int i) const { return i ? make_float2(v.z, v.w) : make_float2(v.x, v.y); }
 };
-template <class T>
-__device__ __forceinline__ float largest(const Raw4<T>& v)
+// An aligned vector on its way to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_vector(void* dst, const void* src)
 {
-    const float2 a = v.pair(0), b = v.pair(1);
-    return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+    if (KIVI_IN_RANGE(src, BYTES)) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+        if constexpr (BYTES == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(src) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(src) : "memory");
+    }
+}
+// The largest logit of U vectors, NaN apart.
+template <class T, int U>
+__device__ __forceinline__ float largest(const Raw4<T> (&v)[U])
+{
+    if constexpr (std::is_same<T, float>::value) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(fmaxf(m, fmaxf(v[u].v.x, v[u].v.y)), fmaxf(v[u].v.z, v[u].v.w));
+        return m;
+    } else {
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        T2 m = *reinterpret_cast<const T2*>(&v[0].v.x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u)
+                m = __hmax2(m, *reinterpret_cast<const T2*>(&v[u].v.x));
+            m = __hmax2(m, *reinterpret_cast<const T2*>(&v[u].v.y));
+        }
+        const float a = to_float(m.x), b = to_float(m.y);
+        return fmaxf(fmaxf(a, b), -INFINITY);  // -infinity for NaN alone
+    }
 }
 template <class T>
 __device__ __forceinline__ F2 pair2(const Raw4<T>& v, int i)
@@ -175,9 +217,6 @@ __device__ __forceinline__ int where(const Raw4<T>& v, float m, int x, int none)
     const float2 a = v.pair(0), b = v.pair(1);
     return a.x == m ? x : a.y == m ? x + 1 : b.x == m ? x + 2 : b.y == m ? x + 3 : none;
 }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(float x) { return x; }
 
 // A largest logit, the sum of weights relative to it, and where it is first met
 // (found for temperature 0 alone).
@@ -186,13 +225,17 @@ struct Stat {
     int first;
 };
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+// Whole numbers in the order of finite and infinite fp32 values.
+__device__ __forceinline__ int ordered(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
 // Of all lanes.
 __device__ __forceinline__ Stat join(Stat s, Scale c, bool greedy)
 {
-    float m = s.m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int top = __reduce_max_sync(0xffffffffu, ordered(s.m + 0.0f));
+    const float m = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
     float l = s.l * weight(s.m - reference(m), c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -203,146 +246,197 @@ __device__ __forceinline__ Stat join(Stat s, Scale c, bool greedy)
     return {m, l, first};
 }
 
-struct ProbsSmem {
-    Stat warp[kProbsWarps], slot[kProbsCluster];
-};
-
 // A cluster per row; CTA r takes the row's vectors of four logits [r per, (r + 1) per),
-// the last one also the up to three logits after them.  The first NV vectors of a
-// thread stay in registers, what lies beyond is read again.  The order of a row's sum
-// does not depend on where the row lies.
-template <class T, int NV>
-__global__ void __launch_bounds__(kProbsThreads, 2)
-token_probs_kernel(ProbsArgs a, int per)
+// the last one also the up to three logits after them.  The first `room` vectors of a
+// CTA stay in its shared memory, what lies beyond is read again.  The order of a row's
+// sum does not depend on where the row lies.
+template <class T>
+__global__ void __launch_bounds__(kProbsThreads, kProbsCtas)
+token_probs_kernel(ProbsArgs a, int per, int room)
 {
-    __shared__ ProbsSmem sm;
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    __shared__ Stat s_stat[kProbsCluster * kProbsWarps];  // of all warps of the cluster
+    Raw4<T>* const kept = reinterpret_cast<Raw4<T>*>(s_raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = (int)(blockIdx.x / C), b = row / a.N, i = row % a.N;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, V = a.V;
+    auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
     // Every CTA comes to both barriers and does the same between them whatever it
     // reads; one of a row that is left as it is has no logits.
     const bool left = a.n_rows && i >= ldg_checked(a.n_rows + b);
-    auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
     const T* src = static_cast<const T*>(a.logits) + b * a.batch_stride + i * a.row_stride;
     float* dst = a.probs + (size_t)row * V;
-    const int nvec = V / 4;
-    const int j0 = left ? nvec : min(rank * per, nvec), j1 = min(j0 + per, nvec);
-    const bool aligned = ((uintptr_t)src & (4 * sizeof(T) - 1)) == 0;
-    auto load = [&](int j) {
-        Raw4<T> v;
-        if (j >= j1)
-            v.clear();
-        else if (aligned)
-            v.load(src + 4 * j);
-        else
-            v.load_each(src + 4 * j);
-        return v;
-    };
-    Raw4<T> keep[NV];
-#pragma unroll
-    for (int r = 0; r < NV; ++r)
-        keep[r] = load(j0 + tid + r * kProbsThreads);
+    const int nvec = V / 4, j0 = left ? nvec : min(rank * per, nvec), j1 = min(j0 + per, nvec), jr = min(j0 + room, j1);
+    const int mis = (int)(((uintptr_t)src / sizeof(T)) & 3);  // logits past an aligned vector
+    if (mis == 0) {
+#pragma unroll 4
+        for (int j = j0 + tid; j < jr; j += kProbsThreads)
+            copy_vector<Raw4<T>::BYTES>(kept + (j - j0), src + 4 * j);
+    } else {
+#pragma unroll 4
+        for (int j = j0 + tid; j < jr; j += kProbsThreads) {
+            Raw4<T> v;
+            if (j > 0 && 4 * j + 8 - mis <= V)
+                v.load_shifted(src + 4 * j, mis);
+            else
+                v.load_each(src + 4 * j);
+            kept[j - j0] = v;
+        }
+    }
     const int edge = 4 * nvec + tid;  // one of the logits after the vectors
     const bool has_edge = !left && rank == C - 1 && edge < V;
     const float edge_l = has_edge ? to_float(ldg_checked(src + edge)) : -INFINITY;
     const float temp = a.temperature ? ldg_checked(a.temperature + b) : 1.0f;
     const bool greedy = temp <= 0.0f;
     const Scale c = inverse_temperature(greedy ? 1.0f : temp);
-    Stat s = {edge_l, 0.0f, has_edge ? edge : INT_MAX};
+    // The U vectors of this thread from j on; -infinity past the end of the CTA's.
+    constexpr int U = 4;
+    auto fetch = [&](int j, Raw4<T> (&v)[U]) {
 #pragma unroll
-    for (int r = 0; r < NV; ++r)
-        if (j0 + r * kProbsThreads < j1)
-            s.m = fmaxf(s.m, largest(keep[r]));
-    {
-        const Scale2 c2 = twice(c, reference(s.m));
-        F2 l = weights_sum(pack2(edge_l, -INFINITY), c2);
+        for (int u = 0; u < U; ++u) {
+            const int x = j + u * kProbsThreads;
+            if (x < jr)
+                v[u] = kept[x - j0];
+            else if (x < j1)
+                v[u].load_each(src + 4 * x);
+            else
+                v[u].clear();
+        }
+    };
+    Stat s = {-INFINITY, 0.0f, INT_MAX};
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a thread reads what it copied itself
+    auto take = [&](const Raw4<T> (&v)[U], int j) {
+        const float m = largest(v);
+        if (m > s.m) {
+            s.l *= weight(s.m - m, c);
+            s.m = m;
+            if (greedy) {
+                s.first = INT_MAX;
 #pragma unroll
-        for (int r = 0; r < NV; ++r)
-            if (j0 + r * kProbsThreads < j1) {
-                l = add2(l, weights_sum(pair2(keep[r], 0), c2));
-                l = add2(l, weights_sum(pair2(keep[r], 1), c2));
+                for (int u = U - 1; u >= 0; --u)
+                    s.first = where(v[u], m, 4 * (j + u * kProbsThreads), s.first);
             }
-        s.l = unpack2(l).x + unpack2(l).y;
-    }
-    if (greedy) {
-        s.first = s.m == edge_l ? s.first : INT_MAX;
+        }
+        const Scale2 c2 = twice(c, reference(s.m));
+        F2 l = weights_sum(pair2(v[0], 0), c2);
+        l = add2(l, weights_sum(pair2(v[0], 1), c2));
 #pragma unroll
-        for (int r = 0; r < NV; ++r)
-            s.first = min(s.first, where(keep[r], s.m, 4 * (j0 + tid + r * kProbsThreads), INT_MAX));
+        for (int u = 1; u < U; ++u) {
+            l = add2(l, weights_sum(pair2(v[u], 0), c2));
+            l = add2(l, weights_sum(pair2(v[u], 1), c2));
+        }
+        s.l += unpack2(l).x + unpack2(l).y;
+    };
+    // chunks of all threads' U vectors each that are kept, then the rest
+    const int chunks = (jr - j0) / (U * kProbsThreads), jc = j0 + chunks * U * kProbsThreads;
+#pragma unroll 1
+    for (int j = tid; j < chunks * U * kProbsThreads; j += U * kProbsThreads) {
+        Raw4<T> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = kept[j + u * kProbsThreads];
+        take(v, j0 + j);
     }
-    for (int j = j0 + tid + NV * kProbsThreads; j < j1; j += kProbsThreads) {
-        const Raw4<T> v = load(j);
-        const float m = fmaxf(s.m, largest(v));
-        const int x = where(v, m, 4 * j, INT_MAX);
-        const Scale2 c2 = twice(c, reference(m));
-        const float2 l = unpack2(add2(weights_sum(pair2(v, 0), c2), weights_sum(pair2(v, 1), c2)));
-        s = {m, s.l * weight(s.m - reference(m), c) + (l.x + l.y), m == s.m ? min(s.first, x) : x};
+#pragma unroll 1
+    for (int j = jc + tid; j < j1; j += U * kProbsThreads) {
+        Raw4<T> v[U];
+        fetch(j, v);
+        take(v, j);
+    }
+    if (has_edge) {  // a thread's last logit
+        const float m = fmaxf(s.m, edge_l), r = reference(m);
+        s = {m, s.l * weight(s.m - r, c) + weight(edge_l - r, c), edge_l > s.m ? edge : s.first};
     }
     s = join(s, c, greedy);
-    if (lane == 0)
-        sm.warp[warp] = s;
-    __syncthreads();
-    s = join(lane < kProbsWarps ? sm.warp[lane] : Stat{-INFINITY, 0.0f, INT_MAX}, c, greedy);
     cluster.barrier_wait(std::move(arrived));
-    if (tid < C)
-        cluster.map_shared_rank(&sm, tid)->slot[rank] = s;
+    if (lane < C)
+        cluster.map_shared_rank(s_stat, lane)[rank * kProbsWarps + warp] = s;
     cluster.sync();
-    s = join(lane < C ? sm.slot[lane] : Stat{-INFINITY, 0.0f, INT_MAX}, c, greedy);
+    s = {-INFINITY, 0.0f, INT_MAX};
+    for (int k = lane; k < C * kProbsWarps; k += 32) {
+        const Stat t = s_stat[k];
+        const float m = fmaxf(s.m, t.m), r = reference(m);
+        s = {m, s.l * weight(s.m - r, c) + t.l * weight(t.m - r, c),
+             s.m == t.m ? min(s.first, t.first) : s.m > t.m ? s.first : t.first};
+    }
+    s = join(s, c, greedy);
     // Outputs of vector j of this lane; all lanes have neighbouring vectors.  Where an
-    // aligned vector begins with output `ahead` of them, its end is the next lane's.
+    // aligned vector begins with output AHEAD of them, its end is the next lane's.
     const int ahead = (int)((0 - (uintptr_t)dst / 4) & 3);
-    auto store = [&](int j, F2 p, F2 q) {
+    auto store = [&](auto known, int j, F2 p, F2 q) {
+        constexpr int AHEAD = decltype(known)::value;
         const float2 x = unpack2(p), y = unpack2(q);
-        float4 v = make_float4(x.x, x.y, y.x, y.y);
-        float* to = dst + 4 * j;
-        if (ahead != 0) {  // the same for the whole row
-            const float4 n = make_float4(__shfl_down_sync(0xffffffffu, v.x, 1), __shfl_down_sync(0xffffffffu, v.y, 1),
-                                         __shfl_down_sync(0xffffffffu, v.z, 1), 0.0f);
+        float o[8] = {x.x, x.y, y.x, y.y};
+        bool whole = j < j1;
+        if constexpr (AHEAD > 0) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                o[4 + k] = __shfl_down_sync(0xffffffffu, o[k], 1);
             const bool last = lane == 31 || j + 1 == j1;
-            if (j < j1) {
-                if (lane == 0 || last) {
-                    if (lane == 0 ? true : ahead < 1)
-                        st_checked(to, v.x);
-                    if (lane == 0 ? ahead > 1 || last : last && ahead <= 1)
-                        st_checked(to + 1, v.y);
-                    if (lane == 0 ? ahead > 2 || last : last && ahead <= 2)
-                        st_checked(to + 2, v.z);
-                    if (last)
-                        st_checked(to + 3, v.w);
-                }
-                if (last)
-                    return;
+            if (whole && (lane == 0 || last)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < AHEAD ? lane == 0 : last)
+                        st_checked(dst + 4 * j + k, o[k]);
             }
-            v = ahead == 1 ? make_float4(v.y, v.z, v.w, n.x)
-                           : ahead == 2 ? make_float4(v.z, v.w, n.x, n.y) : make_float4(v.w, n.x, n.y, n.z);
-            to += ahead;
+            whole = whole && !last;
         }
-        if (j < j1 && KIVI_IN_RANGE(to, 16))
-            __stcs(reinterpret_cast<float4*>(to), v);
+        if (whole && KIVI_IN_RANGE(dst + 4 * j + AHEAD, 16))
+            __stcs(reinterpret_cast<float4*>(dst + 4 * j + AHEAD),
+                   make_float4(o[AHEAD], o[AHEAD + 1], o[AHEAD + 2], o[AHEAD + 3]));
+    };
+    auto by_alignment = [&](auto all) {
+        switch (ahead) {
+        case 0: all(std::integral_constant<int, 0>()); break;
+        case 1: all(std::integral_constant<int, 1>()); break;
+        case 2: all(std::integral_constant<int, 2>()); break;
+        default: all(std::integral_constant<int, 3>()); break;
+        }
     };
     if (greedy) {
         const float zero = isnan(s.l) ? s.l : 0.0f, one = s.l == 0.0f ? 0.0f : 1.0f + zero;
-        for (int base = j0; base < j1; base += kProbsThreads) {
-            const int j = base + tid, x = 4 * j;
-            store(j, pack2(x == s.first ? one : zero, x + 1 == s.first ? one : zero),
-                  pack2(x + 2 == s.first ? one : zero, x + 3 == s.first ? one : zero));
-        }
+        by_alignment([&](auto known) {
+#pragma unroll 1
+            for (int base = j0; base < j1; base += kProbsThreads) {
+                const int j = base + tid, x = 4 * j;
+                store(known, j, pack2(x == s.first ? one : zero, x + 1 == s.first ? one : zero),
+                      pack2(x + 2 == s.first ? one : zero, x + 3 == s.first ? one : zero));
+            }
+        });
         if (has_edge)
             st_checked(dst + edge, edge == s.first ? one : zero);
         return;
     }
     const Scale2 c2 = twice(c, reference(s.m));
     const F2 inv = both(s.l == 0.0f ? 0.0f : 1.0f / s.l);  // NaN for a NaN sum
+    if (ahead == 0) {
+        float* to = dst + 4 * (j0 + tid);
+#pragma unroll 1
+        for (int j = tid; j < chunks * U * kProbsThreads; j += U * kProbsThreads, to += 4 * U * kProbsThreads) {
+            Raw4<T> v[U];
 #pragma unroll
-    for (int r = 0; r < NV; ++r)
-        if (j0 + r * kProbsThreads < j1)
-            store(j0 + tid + r * kProbsThreads, weights(pair2(keep[r], 0), c2, inv), weights(pair2(keep[r], 1), c2, inv));
-    for (int base = j0 + NV * kProbsThreads; base < j1; base += kProbsThreads) {
-        const int j = base + tid;
-        const Raw4<T> v = load(j);
-        store(j, weights(pair2(v, 0), c2, inv), weights(pair2(v, 1), c2, inv));
+            for (int u = 0; u < U; ++u)
+                v[u] = kept[j + u * kProbsThreads];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float2 x = unpack2(weights(pair2(v[u], 0), c2, inv)), y = unpack2(weights(pair2(v[u], 1), c2, inv));
+                if (KIVI_IN_RANGE(to + 4 * u * kProbsThreads, 16))
+                    __stcs(reinterpret_cast<float4*>(to + 4 * u * kProbsThreads), make_float4(x.x, x.y, y.x, y.y));
+            }
+        }
     }
+    by_alignment([&](auto known) {
+#pragma unroll 1
+        for (int base = decltype(known)::value == 0 ? jc : j0; base < j1; base += U * kProbsThreads) {
+            Raw4<T> v[U];
+            fetch(base + tid, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                store(known, base + tid + u * kProbsThreads, weights(pair2(v[u], 0), c2, inv),
+                      weights(pair2(v[u], 1), c2, inv));
+        }
+    });
     if (has_edge)
         st_checked(dst + edge, unpack2(weights(both(edge_l), c2, inv)).x);
 }
@@ -355,18 +449,24 @@ static size_t extent(const ProbsArgs& a)
 }
 #endif
 
-template <class T, int NV>
+template <class T>
 static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
 {
+    constexpr int kMost = kProbsBytes / Raw4<T>::BYTES;  // vectors a CTA keeps
+    static int allowed[64];
+    const cudaError_t e = allow_smem(token_probs_kernel<T>, kProbsBytes, allowed);
+    if (e != cudaSuccess)
+        return e;
     const long long rows = (long long)a.B * a.N;
     const int nvec = a.V / 4;
     int C = 1;
-    while (C < kProbsCluster && (nvec > C * NV * kProbsThreads || (rows * C < 2 * sm_count() && nvec > C * kProbsThreads)))
+    while (C < kProbsCluster && (nvec > C * kMost || (rows * C < 2 * sm_count() && nvec > C * kProbsThreads)))
         C *= 2;
-    const int per = ((nvec + C - 1) / C + 31) / 32 * 32;
+    const int per = ((nvec + C - 1) / C + 31) / 32 * 32, room = std::min(per, kMost);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kProbsThreads);
+    cfg.dynamicSmemBytes = (size_t)room * Raw4<T>::BYTES;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -374,7 +474,7 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, token_probs_kernel<T, NV>, a, per);
+    return cudaLaunchKernelEx(&cfg, token_probs_kernel<T>, a, per, room);
 }
 
 cudaError_t launch_token_probs(const ProbsArgs& a, cudaStream_t s)
@@ -382,9 +482,9 @@ cudaError_t launch_token_probs(const ProbsArgs& a, cudaStream_t s)
     KIVI_SET_CHECK_BUFFERS(s, {{a.logits, extent(a)}, {a.temperature, (size_t)a.B * 4}, {a.n_rows, (size_t)a.B * 4},
                                {a.probs, (size_t)a.B * a.N * a.V * 4}});
     switch (a.dtype) {
-    case KIVI_F16: return launch_probs<__half, 16>(a, s);
-    case KIVI_BF16: return launch_probs<__nv_bfloat16, 16>(a, s);
-    default: return launch_probs<float, 8>(a, s);
+    case KIVI_F16: return launch_probs<__half>(a, s);
+    case KIVI_BF16: return launch_probs<__nv_bfloat16>(a, s);
+    default: return launch_probs<float>(a, s);
     }
 }
 
