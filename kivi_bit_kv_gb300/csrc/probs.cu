@@ -20,9 +20,13 @@ namespace kivi {
 
 namespace cg = cooperative_groups;
 
-constexpr int kProbsThreads = 256, kProbsWarps = kProbsThreads / 32, kProbsCtas = 5;
+// 128 threads a CTA, six CTAs an SM.  In us for 512 rows of 131072 bf16 logits (128 x 6;
+// 5 or 7 CTAs are within 1 %): 256 x 5 73, 512 x 2 77, 1024 x 1 84, 64 x 6 76.  A CTA for
+// one row, without the walk over rows, took 74 (256 threads); clusters of four with
+// twice the shared memory 74.
+constexpr int kProbsThreads = 128, kProbsWarps = kProbsThreads / 32, kProbsCtas = 6;
 constexpr int kProbsCluster = 8;    // most CTAs of a row
-constexpr int kProbsBytes = 32768;  // shared memory for a CTA's logits
+constexpr int kProbsBytes = 32768;  // logits a CTA keeps in shared memory
 
 // log2(e) / T as hi + lo with lo > 0, so that a distance of -infinity gives
 // -infinity through both.  An infinite T gives equal weights to all finite logits, a
@@ -134,14 +138,18 @@ struct Raw4 {
         v.x = ldg_checked(q) | (uint32_t)ldg_checked(q + 1) << 16;
         v.y = ldg_checked(q + 2) | (uint32_t)ldg_checked(q + 3) << 16;
     }
-    // From the two aligned vectors that hold them, `mis` logits into the first.
-    __device__ __forceinline__ void load_shifted(const T* p, int mis)
+    // Four of the eight logits of a and b, from number `skip` (1 to 3) on.
+    __device__ __forceinline__ void shifted(const Raw4& a, const Raw4& b, int skip)
     {
-        const uint2* q = reinterpret_cast<const uint2*>(p - mis);
-        const uint2 a = ldg_checked(q), b = ldg_checked(q + 1);
-        const unsigned long long lo = (unsigned long long)a.y << 32 | a.x, hi = (unsigned long long)b.y << 32 | b.x;
-        const unsigned long long w = lo >> (16 * mis) | hi << (64 - 16 * mis);
-        v = make_uint2((uint32_t)w, (uint32_t)(w >> 32));
+        const uint32_t x = skip >= 2 ? a.v.y : a.v.x, y = skip >= 2 ? b.v.x : a.v.y, z = skip >= 2 ? b.v.y : b.v.x;
+        const int bits = skip % 2 * 16;
+        v = make_uint2(__funnelshift_r(x, y, bits), __funnelshift_r(y, z, bits));
+    }
+    __device__ __forceinline__ Raw4 of_next_lane() const
+    {
+        Raw4 r;
+        r.v = make_uint2(__shfl_down_sync(0xffffffffu, v.x, 1), __shfl_down_sync(0xffffffffu, v.y, 1));
+        return r;
     }
     __device__ __forceinline__ void clear()  // to -infinity
     {
@@ -165,22 +173,22 @@ struct Raw4<float> {
     {
         v = make_float4(ldg_checked(p), ldg_checked(p + 1), ldg_checked(p + 2), ldg_checked(p + 3));
     }
-    __device__ __forceinline__ void load_shifted(const float* p, int) { load_each(p); }
     __device__ __forceinline__ void clear() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ float2 pair(int i) const { return i ? make_float2(v.z, v.w) : make_float2(v.x, v.y); }
 };
-// An aligned vector on its way to shared memory.
+// Aligned bytes on their way to shared memory.
 template <int BYTES>
-__device__ __forceinline__ void copy_vector(void* dst, const void* src)
+__device__ __forceinline__ void copy_bytes(void* dst, const void* src)
 {
     if (KIVI_IN_RANGE(src, BYTES)) {
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
         if constexpr (BYTES == 16)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(src) : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(src) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(to), "l"(src), "n"(BYTES) : "memory");
     }
 }
+
 // The largest logit of U vectors, NaN apart.
 template <class T, int U>
 __device__ __forceinline__ float largest(const Raw4<T> (&v)[U])
@@ -246,199 +254,335 @@ __device__ __forceinline__ Stat join(Stat s, Scale c, bool greedy)
     return {m, l, first};
 }
 
-// A cluster per row; CTA r takes the row's vectors of four logits [r per, (r + 1) per),
-// the last one also the up to three logits after them.  The first `room` vectors of a
-// CTA stay in its shared memory, what lies beyond is read again.  The order of a row's
-// sum does not depend on where the row lies.
+// Place of a CTA's vector k in its shared memory: the 32 of a warp are followed by one
+// more, for rows that are not aligned.
+__host__ __device__ constexpr int slot_of(int k) { return k + k / 32; }
+
+// A row's logits as a CTA's threads keep and read them.  A thread reads what it copied
+// itself, so it needs no barrier, and its share of the next row is on its way as soon as
+// its share of this one has been used.
+//   fp32 and aligned rows: slot k holds vector k.
+//   16-bit rows that begin `skip` logits past an aligned vector: slot k holds the aligned
+// vector with the first of vector k's logits; the rest are in the next one, which the
+// next lane has.  The last lane of a warp, and the one with the CTA's last vector, have
+// that in the slot after.
+template <class T>
+struct Kept {
+    Raw4<T>* slots;
+    int j0, count, V;  // first vector of the CTA, vectors kept, logits of a row
+
+    __device__ __forceinline__ static int skip_of(const T* row) { return (int)(((uintptr_t)row / sizeof(T)) & 3); }
+    __device__ __forceinline__ bool reads_slot_after(int k) const { return (threadIdx.x & 31) == 31 || k == count - 1; }
+
+    // an aligned vector of a row from logit x on, of which some may lie outside the row
+    __device__ __forceinline__ void copy_aligned(int slot, const T* row, int x) const
+    {
+        if (x >= 0 && x + 4 <= V) {
+            copy_bytes<Raw4<T>::BYTES>(slots + slot, row + x);
+        } else {
+            T* to = reinterpret_cast<T*>(slots + slot);
+            for (int i = 0; i < 4; ++i)
+                if (x + i >= 0 && x + i < V)
+                    to[i] = ldg_checked(row + x + i);
+        }
+    }
+    // vectors n + tid, n + tid + kProbsThreads .. below end
+    __device__ __forceinline__ void copy(const T* row, int n, int end) const
+    {
+        const int skip = skip_of(row);
+#pragma unroll 4
+        for (int k = n + (int)threadIdx.x; k < end; k += kProbsThreads) {
+            const int x = 4 * (j0 + k);
+            if (skip == 0) {
+                copy_bytes<Raw4<T>::BYTES>(slots + slot_of(k), row + x);
+            } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy_bytes<4>(reinterpret_cast<float*>(slots + slot_of(k)) + i, row + x + i);
+            } else {
+                copy_aligned(slot_of(k), row, x - skip);
+                if (reads_slot_after(k))
+                    copy_aligned(slot_of(k) + 1, row, x - skip + 4);
+            }
+        }
+    }
+    // the same of U vectors from n + tid on, n a multiple of 32, all below count
+    template <int U>
+    __device__ __forceinline__ void copy_chunk(const T* row, int n) const
+    {
+        const int skip = skip_of(row), x = 4 * (j0 + n);
+        // the aligned vectors of the whole chunk lie in the row
+        const bool inside = sizeof(T) == 2 && x >= skip && x + 4 * U * kProbsThreads + 4 - skip <= V;
+        if (skip != 0 && !inside) {
+            copy(row, n, n + U * kProbsThreads);
+            return;
+        }
+        Raw4<T>* to = slots + slot_of(threadIdx.x) + slot_of(n);
+        const T* from = row + x - skip + 4 * (int)threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            copy_bytes<Raw4<T>::BYTES>(to + slot_of(u * kProbsThreads), from + 4 * u * kProbsThreads);
+        if (skip != 0 && (threadIdx.x & 31) == 31)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                copy_bytes<Raw4<T>::BYTES>(to + slot_of(u * kProbsThreads) + 1, from + 4 * u * kProbsThreads + 4);
+    }
+    // U vectors, as above, of a row that needs shifting or of one that does not
+    template <bool SHIFT, int U>
+    __device__ __forceinline__ void read_chunk(int n, int skip, Raw4<T> (&v)[U]) const
+    {
+        const Raw4<T>* from = slots + slot_of(threadIdx.x) + slot_of(n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = from[slot_of(u * kProbsThreads)];
+            if constexpr (SHIFT) {
+                Raw4<T> after = v[u].of_next_lane();
+                if ((threadIdx.x & 31) == 31)
+                    after = from[slot_of(u * kProbsThreads) + 1];
+                v[u].shifted(v[u], after, skip);
+            }
+        }
+    }
+    // vector k < count of the row; called by all lanes, with neighbouring k
+    __device__ __forceinline__ Raw4<T> read(int k, int skip) const
+    {
+        Raw4<T> v = slots[slot_of(k)];
+        if constexpr (sizeof(T) == 2)
+            if (skip != 0) {
+                Raw4<T> after = v.of_next_lane();
+                if (reads_slot_after(k))
+                    after = slots[slot_of(k) + 1];
+                v.shifted(v, after, skip);
+            }
+        return v;
+    }
+};
+
+// Clusters walk over the rows; CTA r takes a row's vectors of four logits [r per,
+// (r + 1) per), the last one also the up to three logits after them.  The first `room`
+// vectors of a CTA stay in its shared memory, what lies beyond is read again.  The order
+// of a row's sum does not depend on where the row lies.
 template <class T>
 __global__ void __launch_bounds__(kProbsThreads, kProbsCtas)
 token_probs_kernel(ProbsArgs a, int per, int room)
 {
+    constexpr int U = 4;  // vectors a thread works on at a time
     extern __shared__ __align__(16) uint8_t s_raw[];
-    __shared__ Stat s_stat[kProbsCluster * kProbsWarps];  // of all warps of the cluster
-    Raw4<T>* const kept = reinterpret_cast<Raw4<T>*>(s_raw);
+    __shared__ Stat s_stat[2][kProbsCluster * kProbsWarps];  // of all warps of the cluster, for two rows in turn
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int row = (int)(blockIdx.x / C), b = row / a.N, i = row % a.N;
+    const int rows = a.B * a.N, stride = (int)(gridDim.x / C);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, V = a.V;
     auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
-    // Every CTA comes to both barriers and does the same between them whatever it
-    // reads; one of a row that is left as it is has no logits.
-    const bool left = a.n_rows && i >= ldg_checked(a.n_rows + b);
-    const T* src = static_cast<const T*>(a.logits) + b * a.batch_stride + i * a.row_stride;
-    float* dst = a.probs + (size_t)row * V;
-    const int nvec = V / 4, j0 = left ? nvec : min(rank * per, nvec), j1 = min(j0 + per, nvec), jr = min(j0 + room, j1);
-    const int mis = (int)(((uintptr_t)src / sizeof(T)) & 3);  // logits past an aligned vector
-    if (mis == 0) {
-#pragma unroll 4
-        for (int j = j0 + tid; j < jr; j += kProbsThreads)
-            copy_vector<Raw4<T>::BYTES>(kept + (j - j0), src + 4 * j);
-    } else {
-#pragma unroll 4
-        for (int j = j0 + tid; j < jr; j += kProbsThreads) {
-            Raw4<T> v;
-            if (j > 0 && 4 * j + 8 - mis <= V)
-                v.load_shifted(src + 4 * j, mis);
-            else
-                v.load_each(src + 4 * j);
-            kept[j - j0] = v;
-        }
-    }
-    const int edge = 4 * nvec + tid;  // one of the logits after the vectors
-    const bool has_edge = !left && rank == C - 1 && edge < V;
-    const float edge_l = has_edge ? to_float(ldg_checked(src + edge)) : -INFINITY;
-    const float temp = a.temperature ? ldg_checked(a.temperature + b) : 1.0f;
-    const bool greedy = temp <= 0.0f;
-    const Scale c = inverse_temperature(greedy ? 1.0f : temp);
-    // The U vectors of this thread from j on; -infinity past the end of the CTA's.
-    constexpr int U = 4;
-    auto fetch = [&](int j, Raw4<T> (&v)[U]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int x = j + u * kProbsThreads;
-            if (x < jr)
-                v[u] = kept[x - j0];
-            else if (x < j1)
-                v[u].load_each(src + 4 * x);
-            else
-                v[u].clear();
-        }
+    const int nvec = V / 4, j0 = min(rank * per, nvec), all = min(per, nvec - j0);
+    const Kept<T> kept = {reinterpret_cast<Raw4<T>*>(s_raw), j0, min(room, all), V};
+    // chunks of all threads' U vectors each that are kept
+    const int chunked = kept.count / (U * kProbsThreads) * (U * kProbsThreads);
+    struct Row {
+        const T* src;
+        bool on;  // there is such a row, and it is not left as it is
+        float temperature;
     };
-    Stat s = {-INFINITY, 0.0f, INT_MAX};
-    asm volatile("cp.async.wait_all;" ::: "memory");  // a thread reads what it copied itself
-    auto take = [&](const Raw4<T> (&v)[U], int j) {
-        const float m = largest(v);
-        if (m > s.m) {
-            s.l *= weight(s.m - m, c);
-            s.m = m;
-            if (greedy) {
-                s.first = INT_MAX;
+    auto row_of = [&](int row) {
+        Row r = {nullptr, row < rows, 1.0f};
+        if (r.on) {
+            const int b = row / a.N, i = row % a.N;
+            r.src = static_cast<const T*>(a.logits) + b * a.batch_stride + i * a.row_stride;
+            r.on = !(a.n_rows && i >= ldg_checked(a.n_rows + b));
+            if (a.temperature)
+                r.temperature = ldg_checked(a.temperature + b);
+        }
+        return r;
+    };
+    Row next = row_of((int)(blockIdx.x / C));
+    if (next.on)
+        kept.copy(next.src, 0, kept.count);
+    cluster.barrier_wait(std::move(arrived));
+    // Every CTA of a cluster comes to the barrier of every row and does the same before
+    // it whatever it reads.
+#pragma unroll 1
+    for (int row = (int)(blockIdx.x / C), turn = 0; row < rows; row += stride, turn ^= 1) {
+        const Row now = next;
+        const T* src = now.src;
+        float* dst = a.probs + (size_t)row * V;
+        next = row_of(row + stride);
+        const int edge = 4 * nvec + tid;  // one of the logits after the vectors
+        const bool has_edge = now.on && rank == C - 1 && edge < V;
+        const float edge_l = has_edge ? to_float(ldg_checked(src + edge)) : -INFINITY;
+        const bool greedy = now.temperature <= 0.0f;
+        const Scale c = inverse_temperature(greedy ? 1.0f : now.temperature);
+        const int skip = Kept<T>::skip_of(src);
+        auto by_shift = [&](auto body) {
+            if (sizeof(T) == 4 || skip == 0)
+                body(std::false_type());
+            else
+                body(std::integral_constant<bool, sizeof(T) == 2>());
+        };
+        // The U vectors of this thread from vector n + tid on: kept, read again, or past
+        // the end: -infinity.
+        auto fetch = [&](int n, Raw4<T> (&v)[U]) {
 #pragma unroll
-                for (int u = U - 1; u >= 0; --u)
-                    s.first = where(v[u], m, 4 * (j + u * kProbsThreads), s.first);
+            for (int u = 0; u < U; ++u) {
+                const int k = n + tid + u * kProbsThreads;
+                v[u] = kept.read(min(k, room - 1), skip);
+                if (k >= kept.count) {
+                    if (k < all)
+                        v[u].load_each(src + 4 * (j0 + k));
+                    else
+                        v[u].clear();
+                }
             }
+        };
+        Stat s = {-INFINITY, 0.0f, INT_MAX};
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        auto take = [&](const Raw4<T> (&v)[U], int n) {
+            const float m = largest(v);
+            if (m > s.m) {
+                s.l *= weight(s.m - m, c);
+                s.m = m;
+                if (greedy) {
+                    s.first = INT_MAX;
+#pragma unroll
+                    for (int u = U - 1; u >= 0; --u)
+                        s.first = where(v[u], m, 4 * (j0 + n + tid + u * kProbsThreads), s.first);
+                }
+            }
+            const Scale2 c2 = twice(c, reference(s.m));
+            F2 l = weights_sum(pair2(v[0], 0), c2);
+            l = add2(l, weights_sum(pair2(v[0], 1), c2));
+#pragma unroll
+            for (int u = 1; u < U; ++u) {
+                l = add2(l, weights_sum(pair2(v[u], 0), c2));
+                l = add2(l, weights_sum(pair2(v[u], 1), c2));
+            }
+            s.l += unpack2(l).x + unpack2(l).y;
+        };
+        if (now.on) {
+            by_shift([&](auto shift) {
+#pragma unroll 1
+                for (int n = 0; n < chunked; n += U * kProbsThreads) {
+                    Raw4<T> v[U];
+                    kept.template read_chunk<decltype(shift)::value>(n, skip, v);
+                    take(v, n);
+                }
+            });
+#pragma unroll 1
+            for (int n = chunked; n < all; n += U * kProbsThreads) {
+                Raw4<T> v[U];
+                fetch(n, v);
+                take(v, n);
+            }
+        }
+        if (has_edge) {  // a thread's last logit
+            const float m = fmaxf(s.m, edge_l), r = reference(m);
+            s = {m, s.l * weight(s.m - r, c) + weight(edge_l - r, c), edge_l > s.m ? edge : s.first};
+        }
+        s = join(s, c, greedy);
+        if (lane < C)
+            cluster.map_shared_rank(&s_stat[turn][0], lane)[rank * kProbsWarps + warp] = s;
+        cluster.sync();
+        static_assert(kProbsCluster * kProbsWarps <= 32, "a lane for each warp of the cluster");
+        s = lane < C * kProbsWarps ? s_stat[turn][lane] : Stat{-INFINITY, 0.0f, INT_MAX};
+        s = join(s, c, greedy);
+        if (!now.on) {
+            if (next.on)
+                kept.copy(next.src, 0, kept.count);
+            continue;
+        }
+        // Outputs of vector k of this lane; all lanes have neighbouring vectors.  Where an
+        // aligned vector begins with output AHEAD of them, its end is the next lane's; the
+        // first lane's outputs before it and the last one's after it go out one by one.
+        auto store = [&](auto known, int k, F2 p, F2 q) {
+            constexpr int AHEAD = decltype(known)::value;
+            const float2 x = unpack2(p), y = unpack2(q);
+            float o[8] = {x.x, x.y, y.x, y.y};
+            float* to = dst + 4 * (j0 + k);
+            bool whole = k < all;
+            if constexpr (AHEAD > 0) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    o[4 + i] = __shfl_down_sync(0xffffffffu, o[i], 1);
+                const bool last = lane == 31 || k + 1 == all;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (whole && (i < AHEAD ? lane == 0 : last))
+                        st_checked(to + i, o[i]);
+                whole = whole && !last;
+            }
+            if (whole && KIVI_IN_RANGE(to + AHEAD, 16))
+                __stcs(reinterpret_cast<float4*>(to + AHEAD), make_float4(o[AHEAD], o[AHEAD + 1], o[AHEAD + 2], o[AHEAD + 3]));
+        };
+        auto by_alignment = [&](auto body) {
+            switch ((0 - (uintptr_t)dst / 4) & 3) {
+            case 0: body(std::integral_constant<int, 0>()); break;
+            case 1: body(std::integral_constant<int, 1>()); break;
+            case 2: body(std::integral_constant<int, 2>()); break;
+            default: body(std::integral_constant<int, 3>()); break;
+            }
+        };
+        if (greedy) {
+            if (next.on)
+                kept.copy(next.src, 0, kept.count);
+            const float zero = isnan(s.l) ? s.l : 0.0f, one = s.l == 0.0f ? 0.0f : 1.0f + zero;
+            by_alignment([&](auto known) {
+#pragma unroll 1
+                for (int n = 0; n < all; n += kProbsThreads) {
+                    const int x = 4 * (j0 + n + tid);
+                    store(known, n + tid, pack2(x == s.first ? one : zero, x + 1 == s.first ? one : zero),
+                          pack2(x + 2 == s.first ? one : zero, x + 3 == s.first ? one : zero));
+                }
+            });
+            if (has_edge)
+                st_checked(dst + edge, edge == s.first ? one : zero);
+            continue;
         }
         const Scale2 c2 = twice(c, reference(s.m));
-        F2 l = weights_sum(pair2(v[0], 0), c2);
-        l = add2(l, weights_sum(pair2(v[0], 1), c2));
-#pragma unroll
-        for (int u = 1; u < U; ++u) {
-            l = add2(l, weights_sum(pair2(v[u], 0), c2));
-            l = add2(l, weights_sum(pair2(v[u], 1), c2));
-        }
-        s.l += unpack2(l).x + unpack2(l).y;
-    };
-    // chunks of all threads' U vectors each that are kept, then the rest
-    const int chunks = (jr - j0) / (U * kProbsThreads), jc = j0 + chunks * U * kProbsThreads;
-#pragma unroll 1
-    for (int j = tid; j < chunks * U * kProbsThreads; j += U * kProbsThreads) {
-        Raw4<T> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = kept[j + u * kProbsThreads];
-        take(v, j0 + j);
-    }
-#pragma unroll 1
-    for (int j = jc + tid; j < j1; j += U * kProbsThreads) {
-        Raw4<T> v[U];
-        fetch(j, v);
-        take(v, j);
-    }
-    if (has_edge) {  // a thread's last logit
-        const float m = fmaxf(s.m, edge_l), r = reference(m);
-        s = {m, s.l * weight(s.m - r, c) + weight(edge_l - r, c), edge_l > s.m ? edge : s.first};
-    }
-    s = join(s, c, greedy);
-    cluster.barrier_wait(std::move(arrived));
-    if (lane < C)
-        cluster.map_shared_rank(s_stat, lane)[rank * kProbsWarps + warp] = s;
-    cluster.sync();
-    s = {-INFINITY, 0.0f, INT_MAX};
-    for (int k = lane; k < C * kProbsWarps; k += 32) {
-        const Stat t = s_stat[k];
-        const float m = fmaxf(s.m, t.m), r = reference(m);
-        s = {m, s.l * weight(s.m - r, c) + t.l * weight(t.m - r, c),
-             s.m == t.m ? min(s.first, t.first) : s.m > t.m ? s.first : t.first};
-    }
-    s = join(s, c, greedy);
-    // Outputs of vector j of this lane; all lanes have neighbouring vectors.  Where an
-    // aligned vector begins with output AHEAD of them, its end is the next lane's.
-    const int ahead = (int)((0 - (uintptr_t)dst / 4) & 3);
-    auto store = [&](auto known, int j, F2 p, F2 q) {
-        constexpr int AHEAD = decltype(known)::value;
-        const float2 x = unpack2(p), y = unpack2(q);
-        float o[8] = {x.x, x.y, y.x, y.y};
-        bool whole = j < j1;
-        if constexpr (AHEAD > 0) {
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                o[4 + k] = __shfl_down_sync(0xffffffffu, o[k], 1);
-            const bool last = lane == 31 || j + 1 == j1;
-            if (whole && (lane == 0 || last)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < AHEAD ? lane == 0 : last)
-                        st_checked(dst + 4 * j + k, o[k]);
-            }
-            whole = whole && !last;
-        }
-        if (whole && KIVI_IN_RANGE(dst + 4 * j + AHEAD, 16))
-            __stcs(reinterpret_cast<float4*>(dst + 4 * j + AHEAD),
-                   make_float4(o[AHEAD], o[AHEAD + 1], o[AHEAD + 2], o[AHEAD + 3]));
-    };
-    auto by_alignment = [&](auto all) {
-        switch (ahead) {
-        case 0: all(std::integral_constant<int, 0>()); break;
-        case 1: all(std::integral_constant<int, 1>()); break;
-        case 2: all(std::integral_constant<int, 2>()); break;
-        default: all(std::integral_constant<int, 3>()); break;
-        }
-    };
-    if (greedy) {
-        const float zero = isnan(s.l) ? s.l : 0.0f, one = s.l == 0.0f ? 0.0f : 1.0f + zero;
+        const F2 inv = both(s.l == 0.0f ? 0.0f : 1.0f / s.l);  // NaN for a NaN sum
         by_alignment([&](auto known) {
+            constexpr int AHEAD = decltype(known)::value;
+            by_shift([&](auto shift) {
+                float* to = dst + 4 * (j0 + tid);
 #pragma unroll 1
-            for (int base = j0; base < j1; base += kProbsThreads) {
-                const int j = base + tid, x = 4 * j;
-                store(known, j, pack2(x == s.first ? one : zero, x + 1 == s.first ? one : zero),
-                      pack2(x + 2 == s.first ? one : zero, x + 3 == s.first ? one : zero));
+                for (int n = 0; n < chunked; n += U * kProbsThreads, to += 4 * U * kProbsThreads) {
+                    Raw4<T> v[U];
+                    kept.template read_chunk<decltype(shift)::value>(n, skip, v);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {  // as `store`, with all vectors there
+                        const float2 x = unpack2(weights(pair2(v[u], 0), c2, inv));
+                        const float2 y = unpack2(weights(pair2(v[u], 1), c2, inv));
+                        float o[8] = {x.x, x.y, y.x, y.y};
+                        float* at = to + 4 * u * kProbsThreads;
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i)
+                            o[4 + i] = __shfl_down_sync(0xffffffffu, o[i], 1);
+                        if constexpr (AHEAD > 0)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (lane == (i < AHEAD ? 0 : 31))
+                                    st_checked(at + i, o[i]);
+                        if ((AHEAD == 0 || lane != 31) && KIVI_IN_RANGE(at + AHEAD, 16))
+                            __stcs(reinterpret_cast<float4*>(at + AHEAD),
+                                   make_float4(o[AHEAD], o[AHEAD + 1], o[AHEAD + 2], o[AHEAD + 3]));
+                    }
+                    if (next.on)  // these slots have been read
+                        kept.template copy_chunk<U>(next.src, n);
+                }
+            });
+#pragma unroll 1
+            for (int n = chunked; n < all; n += U * kProbsThreads) {
+                Raw4<T> v[U];
+                fetch(n, v);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    store(known, n + tid + u * kProbsThreads, weights(pair2(v[u], 0), c2, inv),
+                          weights(pair2(v[u], 1), c2, inv));
+                if (next.on)
+                    kept.copy(next.src, n, min(n + U * kProbsThreads, kept.count));
             }
         });
         if (has_edge)
-            st_checked(dst + edge, edge == s.first ? one : zero);
-        return;
+            st_checked(dst + edge, unpack2(weights(both(edge_l), c2, inv)).x);
     }
-    const Scale2 c2 = twice(c, reference(s.m));
-    const F2 inv = both(s.l == 0.0f ? 0.0f : 1.0f / s.l);  // NaN for a NaN sum
-    if (ahead == 0) {
-        float* to = dst + 4 * (j0 + tid);
-#pragma unroll 1
-        for (int j = tid; j < chunks * U * kProbsThreads; j += U * kProbsThreads, to += 4 * U * kProbsThreads) {
-            Raw4<T> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                v[u] = kept[j + u * kProbsThreads];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float2 x = unpack2(weights(pair2(v[u], 0), c2, inv)), y = unpack2(weights(pair2(v[u], 1), c2, inv));
-                if (KIVI_IN_RANGE(to + 4 * u * kProbsThreads, 16))
-                    __stcs(reinterpret_cast<float4*>(to + 4 * u * kProbsThreads), make_float4(x.x, x.y, y.x, y.y));
-            }
-        }
-    }
-    by_alignment([&](auto known) {
-#pragma unroll 1
-        for (int base = decltype(known)::value == 0 ? jc : j0; base < j1; base += U * kProbsThreads) {
-            Raw4<T> v[U];
-            fetch(base + tid, v);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                store(known, base + tid + u * kProbsThreads, weights(pair2(v[u], 0), c2, inv),
-                      weights(pair2(v[u], 1), c2, inv));
-        }
-    });
-    if (has_edge)
-        st_checked(dst + edge, unpack2(weights(both(edge_l), c2, inv)).x);
 }
 
 #ifdef KIVI_CHECKS
@@ -453,20 +597,21 @@ template <class T>
 static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
 {
     constexpr int kMost = kProbsBytes / Raw4<T>::BYTES;  // vectors a CTA keeps
-    static int allowed[64];
-    const cudaError_t e = allow_smem(token_probs_kernel<T>, kProbsBytes, allowed);
+    constexpr int kMostSmem = (slot_of(kMost - 1) + 2) * Raw4<T>::BYTES;
+    static int allowed[64], resident[64][kProbsCluster + 1];
+    cudaError_t e = allow_smem(token_probs_kernel<T>, kMostSmem, allowed);
     if (e != cudaSuccess)
         return e;
-    const long long rows = (long long)a.B * a.N;
-    const int nvec = a.V / 4;
+    // As few CTAs a row as keep all of it; more where that leaves SMs idle and a thread
+    // has more than two vectors.
+    const int rows = a.B * a.N, nvec = a.V / 4;
     int C = 1;
-    while (C < kProbsCluster && (nvec > C * kMost || (rows * C < 2 * sm_count() && nvec > C * kProbsThreads)))
+    while (C < kProbsCluster && (nvec > C * kMost || ((long long)rows * C < 2 * sm_count() && nvec > C * 2 * kProbsThreads)))
         C *= 2;
-    const int per = ((nvec + C - 1) / C + 31) / 32 * 32, room = std::min(per, kMost);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.gridDim = dim3((unsigned)C);
     cfg.blockDim = dim3(kProbsThreads);
-    cfg.dynamicSmemBytes = (size_t)room * Raw4<T>::BYTES;
+    cfg.dynamicSmemBytes = kMostSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -474,6 +619,21 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    // the clusters that are resident at once, asked for once per device
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess)
+        return e;
+    int clusters = dev < 64 ? __atomic_load_n(&resident[dev][C], __ATOMIC_RELAXED) : 0;
+    if (clusters == 0) {
+        if ((e = cudaOccupancyMaxActiveClusters(&clusters, token_probs_kernel<T>, &cfg)) != cudaSuccess)
+            return e;
+        clusters = std::max(clusters, 1);
+        if (dev < 64)
+            __atomic_store_n(&resident[dev][C], clusters, __ATOMIC_RELAXED);
+    }
+    const int per = ((nvec + C - 1) / C + 31) / 32 * 32, room = std::max(1, std::min(per, kMost));
+    cfg.gridDim = dim3((unsigned)(std::min(rows, clusters) * C));
+    cfg.dynamicSmemBytes = (size_t)(slot_of(room - 1) + 2) * Raw4<T>::BYTES;
     return cudaLaunchKernelEx(&cfg, token_probs_kernel<T>, a, per, room);
 }
 
