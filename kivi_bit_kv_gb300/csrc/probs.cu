@@ -108,19 +108,19 @@ __device__ __forceinline__ F2 weights_sum(F2 l, const Scale2& c)
     return pack2(exp2_ftz(y.x), exp2_ftz(y.y));
 }
 
-// The same times f, with the rounding of the exponent (half a unit of 2^-24 of up to
-// 126) made good: 2^(y + e) = 2^y (1 + e ln 2).  -e is NaN or infinite only where 2^y
-// is 0 or where the row's sum, and so f, is NaN.
-__device__ __forceinline__ F2 weights(F2 l, const Scale2& c, F2 f)
+// The same times f (1 + rest), with the rounding of the exponent (half a unit of 2^-24 of
+// up to 126) made good: 2^(y + e) = 2^y (1 + e ln 2).  -e is NaN or infinite only where
+// 2^y is 0 or where the row's sum, and so f, is NaN.
+__device__ __forceinline__ F2 weights(F2 l, const Scale2& c, F2 f, F2 rest)
 {
     const F2 d = add2(l, c.minus_ref), y = mul2(d, c.hi);
     const float2 e = unpack2(fma2(d, c.minus_lo, fma2(d, c.minus_hi, y)));
     const F2 w = mul2(pack2(exp2_ftz(unpack2(y).x), exp2_ftz(unpack2(y).y)), f);
-    return fma2(w, mul2(pack2(fmaxf(e.x, -1.0f), fmaxf(e.y, -1.0f)), both(-0.693147181f)), w);
+    return fma2(w, fma2(pack2(fmaxf(e.x, -1.0f), fmaxf(e.y, -1.0f)), both(-0.693147181f), rest), w);
 }
 __device__ __forceinline__ float weight(float d, Scale c)
 {
-    return unpack2(weights(both(d), twice(c, 0.0f), both(1.0f))).x;
+    return unpack2(weights(both(d), twice(c, 0.0f), both(1.0f), both(0.0f))).x;
 }
 
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -537,7 +537,10 @@ token_probs_kernel(ProbsArgs a, int per, int room)
             continue;
         }
         const Scale2 c2 = twice(c, reference(s.m));
-        const F2 inv = both(s.l == 0.0f ? 0.0f : 1.0f / s.l);  // NaN for a NaN sum
+        // the sum's inverse, NaN for a NaN sum, and what its rounding left, which would
+        // be the same for all of the row
+        const float inv1 = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+        const F2 inv = both(inv1), rest = both(s.l == 0.0f ? 0.0f : __fmaf_rn(-inv1, s.l, 1.0f));
         by_alignment([&](auto known) {
             constexpr int AHEAD = decltype(known)::value;
             by_shift([&](auto shift) {
@@ -548,8 +551,8 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                     kept.template read_chunk<decltype(shift)::value>(n, skip, v);
 #pragma unroll
                     for (int u = 0; u < U; ++u) {  // as `store`, with all vectors there
-                        const float2 x = unpack2(weights(pair2(v[u], 0), c2, inv));
-                        const float2 y = unpack2(weights(pair2(v[u], 1), c2, inv));
+                        const float2 x = unpack2(weights(pair2(v[u], 0), c2, inv, rest));
+                        const float2 y = unpack2(weights(pair2(v[u], 1), c2, inv, rest));
                         float o[8] = {x.x, x.y, y.x, y.y};
                         float* at = to + 4 * u * kProbsThreads;
 #pragma unroll
@@ -574,14 +577,14 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                 fetch(n, v);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    store(known, n + tid + u * kProbsThreads, weights(pair2(v[u], 0), c2, inv),
-                          weights(pair2(v[u], 1), c2, inv));
+                    store(known, n + tid + u * kProbsThreads, weights(pair2(v[u], 0), c2, inv, rest),
+                          weights(pair2(v[u], 1), c2, inv, rest));
                 if (next.on)
                     kept.copy(next.src, n, min(n + U * kProbsThreads, kept.count));
             }
         });
         if (has_edge)
-            st_checked(dst + edge, unpack2(weights(both(edge_l), c2, inv)).x);
+            st_checked(dst + edge, unpack2(weights(both(edge_l), c2, inv, rest)).x);
     }
 }
 
