@@ -446,15 +446,38 @@ def kivi_append_path(cache, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor
 
 def _rows_ptr(t: torch.Tensor, dtype, name: str, device) -> int:
     """Pointer of an input whose last dimension is contiguous (any other strides)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.get_device() == device.index:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device.index:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _projection(x, y, name: str, shape, out_shape, dtype, device):
+    """Pointer and strides of the projection x, pointer of its output y; zeros for none."""
+    if x is None or y is None:
+        if x is not y:
+            raise ValueError(f"{name}_in and {name} are given together or not at all")
+        return 0, (0, 0, 0), 0
+    if x.shape != shape:
+        _bad_shape(x, name + "_in", shape)
+    if y.shape != out_shape:
+        _bad_shape(y, name, out_shape)
+    st = x.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}_in must have contiguous channels")
+    return _rows_ptr(x, dtype, name + "_in", device), st[:3], _ptr(y, torch.float16, name, device)
+
+
+def _vector(t, n: int, dtype, name: str, device) -> int:
+    """Pointer of an optional vector of n entries; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != (n,):
+        _bad_shape(t, name, (n,))
+    return _ptr(t, dtype, name, device)
 
 
 def kivi_norm_rope(cache, q_in: torch.Tensor | None, k_in: torch.Tensor | None, v_in: torch.Tensor | None,
@@ -483,47 +506,26 @@ def kivi_norm_rope(cache, q_in: torch.Tensor | None, k_in: torch.Tensor | None, 
     if dtype not in _DTYPES:
         raise TypeError(f"projections must be fp16, bf16 or fp32, got {dtype}")
     Hq = q_in.shape[2] if q_in is not None and q_in.dim() == 4 else H
-    ptrs, strides, outs = [], [], []
-    for name, x, y, heads in (("q", q_in, q, Hq), ("k", k_in, k, H), ("v", v_in, v, H)):
-        if x is None or y is None:
-            if x is not y:
-                raise ValueError(f"{name}_in and {name} are given together or not at all")
-            ptrs.append(0)
-            strides += (0, 0, 0)
-            outs.append(0)
-            continue
-        if x.shape != (B, N, heads, D):
-            _bad_shape(x, name + "_in", (B, N, heads, D))
-        if y.shape != (B, heads, N, D):
-            _bad_shape(y, name, (B, heads, N, D))
-        st = x.stride()
-        if st[3] != 1:
-            raise ValueError(f"{name}_in must have contiguous channels")
-        ptrs.append(_rows_ptr(x, dtype, name + "_in", dev))
-        strides += st[:3]
-        outs.append(_ptr(y, torch.float16, name, dev))
-    half = 0 if inv_freq is None else inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    if half < 0:
-        _bad_shape(inv_freq, "inv_freq", ("rot/2",))
-    n_axes = 1
+    shape, out_shape = (B, N, H, D), (B, H, N, D)
+    qp, qs, qo = _projection(q_in, q, "q", (B, N, Hq, D), (B, Hq, N, D), dtype, dev)
+    kp, ks, ko = _projection(k_in, k, "k", shape, out_shape, dtype, dev)
+    vp, vs, vo = _projection(v_in, v, "v", shape, out_shape, dtype, dev)
+    half, fp = 0, 0
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        fp = _vector(inv_freq, half, torch.float32, "inv_freq", dev) if half else 0
+    n_axes, pp = 1, 0
     if pos is not None:
         n_axes = pos.shape[0] if pos.dim() == 3 else 1
         if pos.shape != (B, N) and pos.shape != (n_axes, B, N):
             _bad_shape(pos, "pos", (B, N), ("n_axes", B, N))
-    if axis is not None and axis.shape != (half,):
-        _bad_shape(axis, "axis", (half,))
-    for name, t, n in (("base", base, B), ("n_tok", n_tok, B), ("q_weight", q_weight, D), ("k_weight", k_weight, D)):
-        if t is not None and t.shape != (n,):
-            _bad_shape(t, name, (n,))
+        pp = _ptr(pos, torch.int32, "pos", dev)
+    i32, f32 = torch.int32, torch.float32
     args = _HEADS.pack(
-        Hq, N, _DTYPES[dtype], 2 * half, int(bool(interleaved)), n_axes, eps, 0, *ptrs, *strides,
-        0 if q_weight is None else _ptr(q_weight, torch.float32, "q_weight", dev),
-        0 if k_weight is None else _ptr(k_weight, torch.float32, "k_weight", dev),
-        _ptr(inv_freq, torch.float32, "inv_freq", dev) if half else 0,
-        0 if axis is None or not half else _ptr(axis, torch.int32, "axis", dev),
-        0 if pos is None else _ptr(pos, torch.int32, "pos", dev),
-        0 if base is None else _ptr(base, torch.int32, "base", dev),
-        0 if n_tok is None else _ptr(n_tok, torch.int32, "n_tok", dev), *outs)
+        Hq, N, _DTYPES[dtype], 2 * half, 1 if interleaved else 0, n_axes, eps, 0, qp, kp, vp, *qs, *ks, *vs,
+        _vector(q_weight, D, f32, "q_weight", dev), _vector(k_weight, D, f32, "k_weight", dev), fp,
+        _vector(axis, half, i32, "axis", dev) if half else 0, pp, _vector(base, B, i32, "base", dev),
+        _vector(n_tok, B, i32, "n_tok", dev), qo, ko, vo)
     _call(load().kivi_norm_rope, "kivi_norm_rope", dev, C.byref(cache.desc), args, _raw_stream(stream, dev))
 
 

@@ -519,6 +519,8 @@ int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream)
         return fail(KIVI_EINVAL, "n_axes=%d; valid: 1 .. %d", a->n_axes, KIVI_MAX_AXES);
     if (!(a->eps >= 0.0f) || a->eps > 3.402823466e38f)
         return fail(KIVI_EINVAL, "eps must be finite and >= 0");
+    if (a->reserved != 0)
+        return fail(KIVI_EINVAL, "reserved=%d must be 0", a->reserved);
     if (!a->q_in && !a->k_in && !a->v_in)
         return fail(KIVI_EINVAL, "q_in, k_in and v_in are all NULL");
     if ((st = check_projection(a, "q", a->q_in, a->q_strides, a->q, c->B, a->Hq, a->q_weight)) != KIVI_OK ||

@@ -525,7 +525,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                 kept.copy(next.src, 0, kept.count);
             const float zero = isnan(s.l) ? s.l : 0.0f, one = s.l == 0.0f ? 0.0f : 1.0f + zero;
             by_alignment([&](auto known) {
-#pragma unroll 1
+#pragma unroll 4
                 for (int n = 0; n < all; n += kProbsThreads) {
                     const int x = 4 * (j0 + n + tid);
                     store(known, n + tid, pack2(x == s.first ? one : zero, x + 1 == s.first ? one : zero),

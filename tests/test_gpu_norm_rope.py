@@ -222,3 +222,37 @@ def test_other_stream_and_graph(cuda):
     call(want)
     for x, z in zip(want, held):
         assert torch.equal(x, z)
+
+
+def test_offsets_past_32_bits(cuda):
+    """2.3e9 outputs: the last heads lie past 2^31 elements, 2^32 bytes."""
+    N, H, D = 70001, 128, 256
+    x = torch.randn((1, 1, H, D), device=cuda).half()
+    out = torch.zeros((1, H, N, D), dtype=torch.float16, device=cuda)
+    abi.kivi_norm_rope(small_cache(cuda, 1, H, D), None, None, x.expand(1, N, H, D), None, None, out, None)
+    assert torch.equal(out, x.transpose(1, 2).expand(1, H, N, D))
+
+
+def test_refusals_name_the_argument(cuda):
+    B, N, H, D = 2, 3, 2, 64
+    c = small_cache(cuda, B, H, D)
+    x = torch.zeros((B, N, H, D), dtype=torch.float16, device=cuda)
+    y = torch.zeros((B, H, N, D), dtype=torch.float16, device=cuda)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=cuda)  # noqa: E731
+    f = freqs(D).to(cuda)
+    good = dict(q_in=x, k_in=x, v_in=x, q=y, k=y.clone(), v=y.clone(), inv_freq=f)
+    abi.kivi_norm_rope(c, **good)
+    for bad, kind, needle in (
+            (dict(q=y[:, :1]), ValueError, "q shape"), (dict(k_in=x[:, :2]), ValueError, "k_in shape"),
+            (dict(v=None), ValueError, "v_in and v"), (dict(q=y.float()), TypeError, "q must be"),
+            (dict(k_in=x.float()), TypeError, "k_in must be"), (dict(q=y.transpose(2, 3).contiguous().transpose(2, 3)), ValueError, "q must be contiguous"),
+            (dict(inv_freq=f.double()), TypeError, "inv_freq must be"), (dict(inv_freq=f[:20]), abi.KiviError, "rot=40"),
+            (dict(pos=i(B, 2)), ValueError, "pos shape"), (dict(pos=i(9, B, N)), abi.KiviError, "n_axes=9"),
+            (dict(pos=i(B, N).long()), TypeError, "pos must be"), (dict(axis=i(5)), ValueError, "axis shape"),
+            (dict(base=i(3)), ValueError, "base shape"), (dict(n_tok=i(1)), ValueError, "n_tok shape"),
+            (dict(q_weight=f), ValueError, "q_weight shape"), (dict(eps=-1.0), abi.KiviError, "eps"),
+            (dict(q_in=torch.zeros((B, N, 3, D), dtype=torch.float16, device=cuda),
+                  q=torch.zeros((B, 3, N, D), dtype=torch.float16, device=cuda)), abi.KiviError, "multiple of H"),
+            (dict(q_in=x.cpu()), ValueError, "q_in must be a CUDA tensor")):
+        with pytest.raises(kind, match=needle):
+            abi.kivi_norm_rope(c, **(good | bad))

@@ -164,3 +164,83 @@ def test_a_captured_step_equals_the_eager_one(cuda):
             assert torch.equal(getattr(eager, name), getattr(graphed, name)), name
         for buf in BUFS:
             assert torch.equal(getattr(eager.cache, buf), getattr(graphed.cache, buf)), buf
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {here!r}]
+import torch
+from kivi_bit_kv_gb300 import KiviCache, abi
+dev = torch.device("cuda", 0)
+B, N, H, D, V = 3, 4, 2, 128, 40001
+cache = KiviCache(B, H, D, 2, 2, 32, 32, 64, device=dev)
+g = torch.Generator(device=dev).manual_seed(1)
+x = torch.randn((B, N, H, D), generator=g, device=dev).bfloat16()
+f = (10000.0 ** (-torch.arange(0, D, 2, device=dev) / D)).float()
+logits = torch.randn((B, N, V), generator=g, device=dev)
+parent = (torch.arange(N, device=dev, dtype=torch.int32) - 1).expand(B, N).contiguous()
+tokens = torch.randint(0, V, (B, N), generator=g, device=dev, dtype=torch.int32)
+u = torch.rand((B, N), generator=g, device=dev)
+def buffers():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    return torch.zeros((B, H, N, D), dtype=torch.float16, device=dev), torch.zeros((B, N, V), device=dev), i(B, N), i(B), i(B)
+def step(q, probs, path, counts, nxt):
+    abi.kivi_norm_rope(cache, x, None, None, q, None, None, f)
+    abi.kivi_token_probs(logits, probs)
+    abi.kivi_verify_tree(tokens, parent, u, probs, None, path, counts, nxt)
+held, eager = buffers(), buffers()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step(*held)
+graph.replay()
+step(*eager)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(held, eager))
+assert int(held[3].min()) >= 1
+print("same")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured(cuda):
+    """What a launcher sets up on its first call does not disturb a capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(here), here=here)
+    out = subprocess.run([sys.executable, "-c", code], check=True, capture_output=True, text=True, timeout=300)
+    assert out.stdout.strip() == "same"
+
+
+def test_two_host_threads_on_streams_of_their_own(cuda):
+    """Calls at once from two threads, each with its own inputs, give what they
+    give one after the other."""
+    import threading
+    models = [Model(cuda, *CASES["tree_int4"], seed=33 + i) for i in range(2)]
+    want = []
+    for m in models:
+        m.new_tree()
+        first, cached = m.next.clone(), [getattr(m.cache, b).clone() for b in BUFS]
+        m.step()
+        torch.cuda.synchronize()
+        want.append([getattr(m, n).clone() for n in ("q", "k", "v", "out", "target", "path", "counts", "next")])
+        m.next.copy_(first)
+        for b, t in zip(BUFS, cached):
+            getattr(m.cache, b).copy_(t)
+    torch.cuda.synchronize()
+
+    def work(m):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for i in range(20):
+                abi.kivi_token_probs(m.draft_logits, m.draft, n_rows=m.n)
+            m.step()
+
+    threads = [threading.Thread(target=work, args=(m,)) for m in models]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for m, w in zip(models, want):
+        for name, t in zip(("q", "k", "v", "out", "target", "path", "counts", "next"), w):
+            assert torch.equal(getattr(m, name), t), name

@@ -79,6 +79,32 @@ def test_largest_vocabulary(cuda):
     compare(cuda, *problem(3, 1, 2, 1 << 20, "chain", "sampled", spread=1.0))
 
 
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 127, 129, 1023, 1025, 8191])
+@pytest.mark.parametrize("kind", ["sampled", "best"])
+def test_small_and_odd_vocabularies(cuda, V, kind):
+    compare(cuda, *problem(40 + V, 9, 5, V, "tree", kind))
+
+
+def test_offsets_past_32_bits(cuda):
+    """Rows that begin past 2^31 elements, 2^33 bytes: 2.7e9 probabilities, of which
+    the last sequence's are looked at."""
+    B, N, V = 64, 41, 1 << 20
+    tokens, parent, u, target, _ = problem(29, 1, N, 4099, "tree", "best")
+    rows = torch.zeros((B, N, V), device=cuda)
+    rows[B - 1, :, V - 4099:] = torch.from_numpy(target[0]).to(cuda)
+    full = np.zeros((N, V), np.float32)
+    full[:, V - 4099:] = target[0]
+    ids = [torch.from_numpy(np.ascontiguousarray(np.broadcast_to(x, (B, N)))).to(cuda)
+           for x in (tokens[0] + V - 4099, parent[0], u[0])]
+    path = torch.zeros((B, N), dtype=torch.int32, device=cuda)
+    counts, nxt = (torch.zeros(B, dtype=torch.int32, device=cuda) for _ in range(2))
+    abi.kivi_verify_tree(*ids, rows, None, path, counts, nxt)
+    want, last = _step.verify(tokens[0] + V - 4099, parent[0], u[0], full, None)
+    assert path[B - 1].tolist() == want + [-1] * (N - len(want)) and int(nxt[B - 1]) == last
+    assert int(counts[B - 1]) == len(want)
+    assert counts[:B - 1].eq(1).all() and nxt[:B - 1].eq(-1).all()        # empty rows
+
+
 @pytest.mark.parametrize("kind", ["sampled", "best"])
 def test_ragged_trees(cuda, kind):
     p = problem(21, 8, 10, 777, "tree", kind)

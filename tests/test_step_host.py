@@ -37,7 +37,7 @@ def heads(**kw):
     (dict(dtype=-1), "dtype=-1"), (dict(rot=8), "rot=8"), (dict(rot=144), "rot=144"), (dict(rot=-16), "rot=-16"),
     (dict(n_axes=0), "n_axes=0"), (dict(n_axes=9), "n_axes=9"), (dict(eps=-1e-6), "eps"), (dict(eps=float("nan")), "eps"),
     (dict(eps=float("inf")), "eps"), (dict(q_in=0), "q: an input"), (dict(k=0), "k: an input"),
-    (dict(q_in=0, k_in=0, v_in=0, q=0, k=0, v=0), "all NULL"), (dict(q_in=Q + 8), "q: the input"),
+    (dict(reserved=1), "reserved=1"), (dict(q_in=0, k_in=0, v_in=0, q=0, k=0, v=0), "all NULL"), (dict(q_in=Q + 8), "q: the input"),
     (dict(v=OV + 2), "v: the input"), (dict(qs=(5 * 1536, 1535, 128)), "dimension 1"),
     (dict(ks=(5 * 1536 + 4, 1536, 128)), "dimension 0"), (dict(vs=(5 * 1536, 1536, 132)), "dimension 2"),
     (dict(q_weight=0x90004), "q_weight"), (dict(inv_freq=0), "inv_freq is NULL"), (dict(inv_freq=F + 2), "inv_freq is not"),
