@@ -4,7 +4,8 @@ The compute path is libkivi.so (include/kivi.h), hand-written CUDA for sm_103a:
 prefix encode of keys (per channel) and values (per token), materialize,
 token append with group flush, and decode attention with dequantization fused
 into the loads -- over the whole cache, over chosen key groups, or for a tree of
-drafted tokens.  This package is its thin Python binding; torch provides
+drafted tokens, with what stands before and after the latter: queries, keys and
+values out of the projections, probabilities, and verification.  This package is its thin Python binding; torch provides
 device memory and streams.
 
     from kivi_bit_kv_gb300 import KiviCache, abi
