@@ -408,7 +408,8 @@ int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k,
  * decode loop: queries, keys and values out of a layer's projections, and
  * the accepted path out of the model's logits.  The pages have no counterpart.
  * None of these calls needs a workspace, each is one kernel on `stream`, and the
- * same inputs give the same bits.  Outputs must not overlap inputs.
+ * same inputs give the same bits.  Outputs must not overlap inputs (KIVI_EINVAL where
+ * those are projections or logits, from their first byte to their last).
  */
 
 /* Types of an input tensor. */

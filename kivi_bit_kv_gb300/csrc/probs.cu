@@ -14,6 +14,7 @@
 #include <utility>
 
 #include "kivi_device.cuh"
+#include "kivi_f32x2.cuh"
 #include "kivi_launch.h"
 
 namespace kivi {
@@ -53,42 +54,6 @@ __device__ __forceinline__ float exp2_ftz(float y)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(y));
     return w;
 }
-
-// Two fp32 values in one operation.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pack2(float a, float b)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 a)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 both(float a) { return pack2(a, a); }
 
 // Scale and reference of a row as the loops below use them, twice each.
 struct Scale2 {

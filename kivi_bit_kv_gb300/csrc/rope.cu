@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "kivi_device.cuh"
+#include "kivi_f32x2.cuh"
 #include "kivi_launch.h"
 
 namespace kivi {
@@ -22,37 +23,6 @@ namespace kivi {
 //     16, 2, 1                                        254      51.1
 //     8, 2, 2                                         294      55.3
 constexpr int kRopeWarps = 4, kRopeCtas = 8;
-
-// Two fp32 values in one operation.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pack2(float a, float b)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 a)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 both(float a) { return pack2(a, a); }
-__device__ __forceinline__ F2 minus(F2 a) { return {a.v ^ 0x8000000080000000ull}; }
 
 // One 16-byte vector of channels: VW of them, as pairs of fp32.
 template <class T>

@@ -16,7 +16,7 @@ namespace kivi {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxWarps = 32;  // warps of a CTA
+constexpr int kMaxWarps = 16;  // warps of a CTA
 constexpr int kMaxCluster = 8;
 
 typedef unsigned long long u64;
@@ -62,7 +62,7 @@ __device__ __forceinline__ u64 whole(float r)
     return w.sum();
 }
 
-// The fp32 rounding of the fp64 rounding of 2^42 / z, z < 2^62 (0 for 0).  In fp32 with
+// The fp32 rounding of the fp64 rounding of 2^42 / z, z <= 2^62 (0 for 0).  In fp32 with
 // z as h + l and the quotient as q0 + q1, each in two terms: off by some 2^-46 of it.
 // The rounded sum s is right where what it leaves is not that near half a unit of s;
 // the division in 64 bits, far slower, is left for the rest.  (Below a power of two the
@@ -203,7 +203,7 @@ __device__ __forceinline__ int next_child(const VerifyTree& t, int cur, int from
 }
 
 // Warp w of CTA r sums the run of neighbouring places r (warps of a CTA) + w.
-__global__ void __launch_bounds__(32 * kMaxWarps)
+__global__ void __launch_bounds__(32 * kMaxWarps, 2)
 verify_tree_kernel(VerifyArgs a, int run)
 {
     constexpr int U = 4;

@@ -253,6 +253,7 @@ def test_refusals_name_the_argument(cuda):
             (dict(q_weight=f), ValueError, "q_weight shape"), (dict(eps=-1.0), abi.KiviError, "eps"),
             (dict(q_in=torch.zeros((B, N, 3, D), dtype=torch.float16, device=cuda),
                   q=torch.zeros((B, 3, N, D), dtype=torch.float16, device=cuda)), abi.KiviError, "multiple of H"),
+            (dict(k=x.view(B, H, N, D)), abi.KiviError, "k overlaps"),
             (dict(q_in=x.cpu()), ValueError, "q_in must be a CUDA tensor")):
         with pytest.raises(kind, match=needle):
             abi.kivi_norm_rope(c, **(good | bad))

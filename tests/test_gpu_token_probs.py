@@ -66,6 +66,14 @@ def test_rows_at_any_element(cuda, V, pad, skip, dtype):
     assert torch.equal(out2.transpose(0, 1), out)
 
 
+def test_in_place_is_refused(cuda):
+    x = torch.zeros((2, 3, 1000), device=cuda)
+    with pytest.raises(abi.KiviError, match="overlaps"):
+        abi.kivi_token_probs(x, x)
+    both = torch.zeros(12000, device=cuda)
+    abi.kivi_token_probs(both[:6000].view(2, 3, 1000), both[6000:].view(2, 3, 1000))    # side by side
+
+
 def test_one_row_for_all_by_broadcast(cuda):
     x = torch.randn(4096, device=cuda).half()
     out = torch.zeros((5, 2, 4096), device=cuda)

@@ -40,6 +40,7 @@ def heads(**kw):
     (dict(reserved=1), "reserved=1"), (dict(q_in=0, k_in=0, v_in=0, q=0, k=0, v=0), "all NULL"), (dict(q_in=Q + 8), "q: the input"),
     (dict(v=OV + 2), "v: the input"), (dict(qs=(5 * 1536, 1535, 128)), "dimension 1"),
     (dict(ks=(5 * 1536 + 4, 1536, 128)), "dimension 0"), (dict(vs=(5 * 1536, 1536, 132)), "dimension 2"),
+    (dict(q=Q), "q overlaps input q_in"), (dict(k=Q + 1024), "k overlaps"), (dict(v=Q + 28672 - 16), "v overlaps"),
     (dict(q_weight=0x90004), "q_weight"), (dict(inv_freq=0), "inv_freq is NULL"), (dict(inv_freq=F + 2), "inv_freq is not"),
     (dict(axis=0x90002), "axis"), (dict(pos=0x90001), "pos"), (dict(base=0x90002), "base"), (dict(n_tok=0x90003), "n_tok"),
 ])
@@ -85,6 +86,7 @@ def test_token_probs_refusals(kivi_lib):
                            (dict(l=Q + 2, dtype=abi.KIVI_F32), "logits is not"), (dict(dtype=3), "dtype=3"),
                            (dict(B=0), "B=0"), (dict(N=0), "N=0"), (dict(N=1 << 26), "2^27"), (dict(V=0), "V=0"),
                            (dict(V=abi.KIVI_MAX_VOCAB + 1), "vocabulary"), (dict(t=K + 2), "temperature"),
+                           (dict(p=Q), "probs overlaps"), (dict(p=Q + 11984), "probs overlaps"), (dict(p=Q - 23984), "probs overlaps"),
                            (dict(n=V + 1), "n_rows"), (dict(p=None), "probs is NULL"), (dict(p=OQ + 8), "probs is not")):
         assert f(*(good | change).values(), None) == abi.KIVI_EINVAL, change
         assert needle in abi.kivi_last_error(), abi.kivi_last_error()
