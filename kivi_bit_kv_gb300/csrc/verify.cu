@@ -203,18 +203,27 @@ __device__ __forceinline__ int next_child(const VerifyTree& t, int cur, int from
 }
 
 // Warp w of CTA r sums the run of neighbouring places r (warps of a CTA) + w.
-__global__ void __launch_bounds__(32 * kMaxWarps, 2)
+template <int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH)
 verify_tree_kernel(VerifyArgs a, int run)
 {
-    constexpr int U = 4;
+    constexpr int U = 4;  // lines of a run loaded at a time
     __shared__ VerifySmem sm;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = (int)(blockIdx.x / C), tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    const int threads = blockDim.x, warps = threads / 32, N = a.N, V = a.V;
+    constexpr int threads = TH, warps = TH / 32;
+    const int N = a.N, V = a.V;
     const size_t row0 = (size_t)b * N;
     const bool drawn = a.draft != nullptr;
     auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
+    const int g = rank * warps + warp;
+    const int y0 = (int)min((long long)g * run, (long long)V + 3), y1 = y0 + run;
+    auto row_of = [&](int node) {
+        const size_t at = (row0 + node) * V;
+        const int off = (int)(at & 3);
+        return Row{a.target + at - off, drawn ? a.draft + at - off : nullptr, off, off + V};
+    };
     if (rank == 0) {
         VerifyTree& t = sm.tree;
         const int n = a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), N) : N;
@@ -249,13 +258,6 @@ verify_tree_kernel(VerifyArgs a, int run)
         }
     cluster.sync();
     const VerifyTree& t = sm.tree;
-    const int g = rank * warps + warp;
-    const int y0 = (int)min((long long)g * run, (long long)V + 3), y1 = y0 + run;
-    auto row_of = [&](int node) {
-        const size_t at = (row0 + node) * V;
-        const int off = (int)(at & 3);
-        return Row{a.target + at - off, drawn ? a.draft + at - off : nullptr, off, off + V};
-    };
     int pass = 0;
     // Sum of the runs before run n in the last pass.
     auto runs_before = [&](int n) {
@@ -489,7 +491,8 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_tree_kernel, a, run);
+    return threads == 512 ? cudaLaunchKernelEx(&cfg, verify_tree_kernel<512>, a, run)
+                          : cudaLaunchKernelEx(&cfg, verify_tree_kernel<256>, a, run);
 }
 
 #ifdef KIVI_CHECKS
