@@ -339,6 +339,9 @@ token_probs_kernel(ProbsArgs a, int per, int room)
     const int rows = a.B * a.N, stride = (int)(gridDim.x / C);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, V = a.V;
     auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
+    // A programmatic dependent: its CTAs may be scheduled while the kernel before it ends,
+    // and read and write nothing until that is done.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int nvec = V / 4, j0 = min(rank * per, nvec), all = min(per, nvec - j0);
     const Kept<T> kept = {reinterpret_cast<Raw4<T>*>(s_raw), j0, min(room, all), V};
     // chunks of all threads' U vectors each that are kept
@@ -581,12 +584,14 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
     cfg.blockDim = dim3(kProbsThreads);
     cfg.dynamicSmemBytes = kMostSmem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     // the clusters that are resident at once, asked for once per device
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess)

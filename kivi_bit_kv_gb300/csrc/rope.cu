@@ -116,6 +116,9 @@ norm_rope_kernel(const __grid_constant__ RopeArgs a)
     constexpr int VW = Vec<T>::VW, NV = 16 / VW, HW = VW / 2;
     __shared__ __align__(16) float s_cos[kRopeWarps][D / 2];
     __shared__ __align__(16) float s_sin[kRopeWarps][D / 2];
+    // A programmatic dependent: its CTAs may be scheduled while the kernel before it ends,
+    // and read and write nothing until that is done.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const long long w = (long long)blockIdx.x * kRopeWarps + warp;
     const int tokens = a.B * a.N;
@@ -268,11 +271,17 @@ static cudaError_t launch_rope(const kivi_cache& c, const kivi_heads& h, cudaStr
     a.per = (int)std::max(1ll, std::min((long long)steps, tokens * steps / (128ll * sm_count())));
     const long long warps = tokens * ((steps + a.per - 1) / a.per);
     const unsigned grid = (unsigned)((warps + kRopeWarps - 1) / kRopeWarps);
-    if (h.interleaved)
-        norm_rope_kernel<T, D, true><<<grid, 32 * kRopeWarps, 0, s>>>(a);
-    else
-        norm_rope_kernel<T, D, false><<<grid, 32 * kRopeWarps, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(32 * kRopeWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return h.interleaved ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, D, true>, a)
+                         : cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, D, false>, a);
 }
 
 template <class T>

@@ -217,6 +217,9 @@ verify_tree_kernel(VerifyArgs a, int run)
     const size_t row0 = (size_t)b * N;
     const bool drawn = a.draft != nullptr;
     auto arrived = cluster.barrier_arrive();  // this CTA's shared memory may be written
+    // A programmatic dependent: its CTAs may be scheduled while the kernel before it ends,
+    // and read and write nothing until that is done.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int g = rank * warps + warp;
     const int y0 = (int)min((long long)g * run, (long long)V + 3), y1 = y0 + run;
     auto row_of = [&](int node) {
@@ -485,12 +488,14 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, cudaStream_t s)
     cfg.gridDim = dim3((unsigned)(a.B * C));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     return threads == 512 ? cudaLaunchKernelEx(&cfg, verify_tree_kernel<512>, a, run)
                           : cudaLaunchKernelEx(&cfg, verify_tree_kernel<256>, a, run);
 }

@@ -244,3 +244,49 @@ def test_two_host_threads_on_streams_of_their_own(cuda):
     for m, w in zip(models, want):
         for name, t in zip(("q", "k", "v", "out", "target", "path", "counts", "next"), w):
             assert torch.equal(getattr(m, name), t), name
+
+
+def test_a_captured_fork_and_join(cuda):
+    """Calls on two branches of a graph, joined before a third, between kernels of
+    other libraries: every call waits for all that it reads."""
+    B, N, V = 4, 5, 40000
+    g = torch.Generator(device=cuda).manual_seed(35)
+    logits, draft_logits = (torch.randn((B, N, V), generator=g, device=cuda) for _ in range(2))
+    tokens = torch.randint(0, V, (B, N), generator=g, device=cuda, dtype=torch.int32)
+    parent = torch.tensor([-1, 0, 0, 1, 2], dtype=torch.int32, device=cuda).expand(B, N).contiguous()
+    u = torch.rand((B, N), generator=g, device=cuda)
+
+    def buffers():
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device=cuda)  # noqa: E731
+        return [torch.zeros((B, N, V), device=cuda) for _ in range(4)] + [z(B, N), z(B), z(B)]
+
+    def run(b, fork):
+        x, y, p, q, path, counts, nxt = b
+        side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+        if fork:
+            side.wait_stream(main)
+        with torch.cuda.stream(side if fork else main):
+            torch.mul(draft_logits, 3.0, out=y)
+            abi.kivi_token_probs(y, q)
+        torch.mul(logits, 3.0, out=x)
+        abi.kivi_token_probs(x, p)
+        if fork:
+            main.wait_stream(side)
+        abi.kivi_verify_tree(tokens, parent, u, p, q, path, counts, nxt)
+        counts.add_(100)
+        p.zero_()
+        q.zero_()
+
+    eager, held = buffers(), buffers()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(held, True)
+    for _ in range(20):
+        u.uniform_()
+        logits.normal_()
+        run(eager, False)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager[4:], held[4:]):
+            assert torch.equal(a, b)
+        assert int(held[5].min()) >= 101
