@@ -12,11 +12,11 @@ namespace kivi {
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
-// Lets `kern` use `bytes` of dynamic shared memory; asks the runtime once per
-// device (`done`: a static of the launcher).  `bytes` is a constant of the
-// kernel, so that host threads that race ask for the same.
+// Sets an attribute of `kern`; asks the runtime once per device (`done`: a static of
+// the launcher).  `value` is a constant of the kernel, so that host threads that
+// race ask for the same.
 template <class Kern>
-inline cudaError_t allow_smem(Kern kern, int bytes, int (&done)[64])
+inline cudaError_t set_attribute_once(Kern kern, cudaFuncAttribute attribute, int value, int (&done)[64])
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -24,10 +24,22 @@ inline cudaError_t allow_smem(Kern kern, int bytes, int (&done)[64])
         return e;
     if (dev < 64 && __atomic_load_n(&done[dev], __ATOMIC_RELAXED))
         return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(kern, attribute, value);
     if (e == cudaSuccess && dev < 64)
         __atomic_store_n(&done[dev], 1, __ATOMIC_RELAXED);
     return e;
+}
+// Lets `kern` use `bytes` of dynamic shared memory.
+template <class Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, int (&done)[64])
+{
+    return set_attribute_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
+}
+// Lets `kern` run in clusters of more than eight CTAs.
+template <class Kern>
+inline cudaError_t allow_wide_clusters(Kern kern, int (&done)[64])
+{
+    return set_attribute_once(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done);
 }
 
 // Number of decode chunks (one CTA per KV head and chunk) that cover Tmax.

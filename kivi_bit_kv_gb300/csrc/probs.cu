@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 // one row, without the walk over rows, took 74 (256 threads); clusters of four with
 // twice the shared memory 74.
 constexpr int kProbsThreads = 128, kProbsWarps = kProbsThreads / 32, kProbsCtas = 6;
-constexpr int kProbsCluster = 8;    // most CTAs of a row
+constexpr int kProbsCluster = 16;   // most CTAs of a row
 constexpr int kProbsBytes = 32768;  // logits a CTA keeps in shared memory
 
 // log2(e) / T as hi + lo with lo > 0, so that a distance of -infinity gives
@@ -449,8 +449,14 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         if (lane < C)
             cluster.map_shared_rank(&s_stat[turn][0], lane)[rank * kProbsWarps + warp] = s;
         cluster.sync();
-        static_assert(kProbsCluster * kProbsWarps <= 32, "a lane for each warp of the cluster");
+        static_assert(kProbsCluster * kProbsWarps <= 64, "a lane for two warps of the cluster");
         s = lane < C * kProbsWarps ? s_stat[turn][lane] : Stat{-INFINITY, 0.0f, INT_MAX};
+        if (lane + 32 < C * kProbsWarps) {
+            const Stat t = s_stat[turn][lane + 32];
+            const float m = fmaxf(s.m, t.m), r = reference(m);
+            s = {m, s.l * weight(s.m - r, c) + t.l * weight(t.m - r, c),
+                 s.m == t.m ? min(s.first, t.first) : s.m > t.m ? s.first : t.first};
+        }
         s = join(s, c, greedy);
         if (!now.on) {
             if (next.on)
@@ -569,15 +575,19 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
 {
     constexpr int kMost = kProbsBytes / Raw4<T>::BYTES;  // vectors a CTA keeps
     constexpr int kMostSmem = (slot_of(kMost - 1) + 2) * Raw4<T>::BYTES;
-    static int allowed[64], resident[64][kProbsCluster + 1];
+    static int allowed[64], wide[64], resident[64][kProbsCluster + 1];
     cudaError_t e = allow_smem(token_probs_kernel<T>, kMostSmem, allowed);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess || (e = allow_wide_clusters(token_probs_kernel<T>, wide)) != cudaSuccess)
         return e;
-    // As few CTAs a row as keep all of it; more where that leaves SMs idle and a thread
-    // has more than two vectors.
+    // As few CTAs a row as keep all of it; up to eight where fewer leave SMs idle and a
+    // thread has more than two vectors; sixteen also where each of them has an SM.  In us
+    // with eight and with sixteen, fp32 rows of 131072: 8 rows 7.7 and 5.4, 512 rows (half
+    // of which eight would read again) 99.6 and 92.5; 32 bf16 rows 7.4 and 8.2.
     const int rows = a.B * a.N, nvec = a.V / 4;
     int C = 1;
-    while (C < kProbsCluster && (nvec > C * kMost || ((long long)rows * C < 2 * sm_count() && nvec > C * 2 * kProbsThreads)))
+    while (C < kProbsCluster &&
+           (nvec > C * kMost || (nvec > C * 2 * kProbsThreads &&
+                                 (C < 8 ? (long long)rows * C < 2 * sm_count() : (long long)rows * 2 * C <= sm_count()))))
         C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)C);
