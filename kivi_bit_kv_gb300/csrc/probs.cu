@@ -103,6 +103,7 @@ struct Raw4 {
         v.x = ldg_checked(q) | (uint32_t)ldg_checked(q + 1) << 16;
         v.y = ldg_checked(q + 2) | (uint32_t)ldg_checked(q + 3) << 16;
     }
+    __device__ __forceinline__ void load(const T* p) { v = ldg_checked(reinterpret_cast<const uint2*>(p)); }
     // Four of the eight logits of a and b, from number `skip` (1 to 3) on.
     __device__ __forceinline__ void shifted(const Raw4& a, const Raw4& b, int skip)
     {
@@ -138,6 +139,7 @@ struct Raw4<float> {
     {
         v = make_float4(ldg_checked(p), ldg_checked(p + 1), ldg_checked(p + 2), ldg_checked(p + 3));
     }
+    __device__ __forceinline__ void load(const float* p) { v = ld_nc_f4(p); }
     __device__ __forceinline__ void clear() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ float2 pair(int i) const { return i ? make_float2(v.z, v.w) : make_float2(v.x, v.y); }
 };
@@ -394,10 +396,12 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                 const int k = n + tid + u * kProbsThreads;
                 v[u] = kept.read(min(k, room - 1), skip);
                 if (k >= kept.count) {
-                    if (k < all)
-                        v[u].load_each(src + 4 * (j0 + k));
-                    else
+                    if (k >= all)
                         v[u].clear();
+                    else if (skip == 0)
+                        v[u].load(src + 4 * (j0 + k));
+                    else
+                        v[u].load_each(src + 4 * (j0 + k));
                 }
             }
         };
@@ -590,29 +594,35 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
                                  (C < 8 ? (long long)rows * C < 2 * sm_count() : (long long)rows * 2 * C <= sm_count()))))
         C *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)C);
     cfg.blockDim = dim3(kProbsThreads);
     cfg.dynamicSmemBytes = kMostSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 2;
-    // the clusters that are resident at once, asked for once per device
-    int dev = 0;
+    // The clusters that are resident at once, asked for once per device; where none of
+    // sixteen CTAs is, smaller ones do.
+    int dev = 0, clusters = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess)
         return e;
-    int clusters = dev < 64 ? __atomic_load_n(&resident[dev][C], __ATOMIC_RELAXED) : 0;
-    if (clusters == 0) {
-        if ((e = cudaOccupancyMaxActiveClusters(&clusters, token_probs_kernel<T>, &cfg)) != cudaSuccess)
-            return e;
-        clusters = std::max(clusters, 1);
-        if (dev < 64)
-            __atomic_store_n(&resident[dev][C], clusters, __ATOMIC_RELAXED);
+    for (;; C /= 2) {
+        at[0].val.clusterDim.x = (unsigned)C;
+        cfg.gridDim = dim3((unsigned)C);
+        clusters = dev < 64 ? __atomic_load_n(&resident[dev][C], __ATOMIC_RELAXED) : 0;
+        if (clusters == 0) {
+            if ((e = cudaOccupancyMaxActiveClusters(&clusters, token_probs_kernel<T>, &cfg)) != cudaSuccess)
+                return e;
+            if (clusters == 0)
+                clusters = C > 8 ? -1 : 1;
+            if (dev < 64)
+                __atomic_store_n(&resident[dev][C], clusters, __ATOMIC_RELAXED);
+        }
+        if (clusters > 0)
+            break;
     }
     const int per = ((nvec + C - 1) / C + 31) / 32 * 32, room = std::max(1, std::min(per, kMost));
     cfg.gridDim = dim3((unsigned)(std::min(rows, clusters) * C));
