@@ -29,23 +29,35 @@ constexpr int kProbsThreads = 128, kProbsWarps = kProbsThreads / 32, kProbsCtas 
 constexpr int kProbsCluster = 16;   // most CTAs of a row
 constexpr int kProbsBytes = 32768;  // logits a CTA keeps in shared memory
 
-// log2(e) / T as hi + lo with lo > 0, so that a distance of -infinity gives
-// -infinity through both.  An infinite T gives equal weights to all finite logits, a
-// tiny one only to the largest: hi stays between the smallest normal and the largest
-// finite number.  NaN for a NaN T.
+// A distance d = l - ref <= 0 of a logit from the largest weighs 2^(d log2(e) / T).  Where T
+// is far from 1 the distance is formed as `unit` times itself, unit a power of two, and
+// log2(e) / (unit T) taken, so that neither leaves the range of fp32: from 2^100 on logits
+// near both ends of the range have a finite distance, below 2^-100 the quotient is finite.
+// log2(e) / (unit T) as hi + lo with lo > 0, so that a distance of -infinity gives -infinity
+// through both.  With an infinite T all finite distances (below 2^65 in their unit) weigh
+// 2^-0.  NaN for a NaN T.
 struct Scale {
-    float hi, lo;
+    float hi, lo, unit;
 };
 __device__ __forceinline__ Scale inverse_temperature(float T)
 {
     constexpr double kLog2e = 1.44269504088896340736;
     constexpr float L = 1.44269502f;  // below log2(e)
     static_assert((double)L < kLog2e, "");
-    if (isinf(T))
-        return {0x1p-126f, 0x1p-149f};
-    const float hi = fmaxf(__fdiv_rz(L, T), 0x1p-126f);
-    const float lo = __fdiv_rn(__fmaf_rn(-hi, T, L) + (float)(kLog2e - (double)L), T);
-    return {isnan(T) ? T : hi, fminf(fmaxf(lo, 0x1p-149f), hi * 0x1p-22f)};
+    const float unit = T >= 0x1p100f ? 0x1p-64f : T < 0x1p-100f ? 0x1p64f : 1.0f, t = T * unit;
+    const float hi = __fdiv_rz(L, t);
+    const float lo = __fdiv_rn(__fmaf_rn(-hi, t, L) + (float)(kLog2e - (double)L), t);
+    return isinf(T) ? Scale{0x1p-126f, 0x1p-149f, unit} : Scale{hi, fmaxf(lo, 0x1p-149f), unit};
+}
+// Distances from ref as l unit + minus.  A large unit is 1 where l would overflow: distances
+// other than 0 are 2^36 or more there, and weigh 0.
+struct Ref {
+    float unit, minus;
+};
+__device__ __forceinline__ Ref ref_at(const Scale& c, float ref)
+{
+    const float unit = fabsf(ref) < 0x1p60f ? c.unit : fminf(c.unit, 1.0f);
+    return {unit, -ref * unit};
 }
 
 __device__ __forceinline__ float exp2_ftz(float y)
@@ -57,18 +69,19 @@ __device__ __forceinline__ float exp2_ftz(float y)
 
 // Scale and reference of a row as the loops below use them, twice each.
 struct Scale2 {
-    F2 hi, lo, minus_ref, minus_hi, minus_lo;
+    F2 hi, lo, unit, minus_ref, minus_hi, minus_lo;
+    __device__ __forceinline__ F2 distance(F2 l) const { return fma2(l, unit, minus_ref); }
 };
-__device__ __forceinline__ Scale2 twice(Scale c, float ref)
+__device__ __forceinline__ Scale2 twice(const Scale& c, Ref ref)
 {
-    return {both(c.hi), both(c.lo), both(-ref), both(-c.hi), both(-c.lo)};
+    return {both(c.hi), both(c.lo), both(ref.unit), both(ref.minus), both(-c.hi), both(-c.lo)};
 }
 
 // 2^(d (hi + lo)) of distances d = l - ref <= 0 from the largest logit; NaN for a NaN
 // d, 0 for -infinity.  For sums, whose terms' roundings cancel.
 __device__ __forceinline__ F2 weights_sum(F2 l, const Scale2& c)
 {
-    const F2 d = add2(l, c.minus_ref);
+    const F2 d = c.distance(l);
     const float2 y = unpack2(fma2(d, c.lo, mul2(d, c.hi)));
     return pack2(exp2_ftz(y.x), exp2_ftz(y.y));
 }
@@ -78,14 +91,14 @@ __device__ __forceinline__ F2 weights_sum(F2 l, const Scale2& c)
 // 2^y is 0 or where the row's sum, and so f, is NaN.
 __device__ __forceinline__ F2 weights(F2 l, const Scale2& c, F2 f, F2 rest)
 {
-    const F2 d = add2(l, c.minus_ref), y = mul2(d, c.hi);
+    const F2 d = c.distance(l), y = mul2(d, c.hi);
     const float2 e = unpack2(fma2(d, c.minus_lo, fma2(d, c.minus_hi, y)));
     const F2 w = mul2(pack2(exp2_ftz(unpack2(y).x), exp2_ftz(unpack2(y).y)), f);
     return fma2(w, fma2(pack2(fmaxf(e.x, -1.0f), fmaxf(e.y, -1.0f)), both(-0.693147181f), rest), w);
 }
-__device__ __forceinline__ float weight(float d, Scale c)
+__device__ __forceinline__ float weight(float l, float ref, const Scale& c)
 {
-    return unpack2(weights(both(d), twice(c, 0.0f), both(1.0f), both(0.0f))).x;
+    return unpack2(weights(both(l), twice(c, ref_at(c, ref)), both(1.0f), both(0.0f))).x;
 }
 
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -207,11 +220,11 @@ __device__ __forceinline__ int ordered(float x)
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 // Of all lanes.
-__device__ __forceinline__ Stat join(Stat s, Scale c, bool greedy)
+__device__ __forceinline__ Stat join(Stat s, const Scale& c, bool greedy)
 {
     const int top = __reduce_max_sync(0xffffffffu, ordered(s.m + 0.0f));
     const float m = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-    float l = s.l * weight(s.m - reference(m), c);
+    float l = s.l * weight(s.m, reference(m), c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -406,12 +419,14 @@ token_probs_kernel(ProbsArgs a, int per, int room)
             }
         };
         Stat s = {-INFINITY, 0.0f, INT_MAX};
+        Ref ref = ref_at(c, reference(s.m));
         asm volatile("cp.async.wait_all;" ::: "memory");
         auto take = [&](const Raw4<T> (&v)[U], int n) {
             const float m = largest(v);
             if (m > s.m) {
-                s.l *= weight(s.m - m, c);
+                s.l *= weight(s.m, m, c);
                 s.m = m;
+                ref = ref_at(c, m);
                 if (greedy) {
                     s.first = INT_MAX;
 #pragma unroll
@@ -419,7 +434,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                         s.first = where(v[u], m, 4 * (j0 + n + tid + u * kProbsThreads), s.first);
                 }
             }
-            const Scale2 c2 = twice(c, reference(s.m));
+            const Scale2 c2 = twice(c, ref);
             F2 l = weights_sum(pair2(v[0], 0), c2);
             l = add2(l, weights_sum(pair2(v[0], 1), c2));
 #pragma unroll
@@ -447,7 +462,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         }
         if (has_edge) {  // a thread's last logit
             const float m = fmaxf(s.m, edge_l), r = reference(m);
-            s = {m, s.l * weight(s.m - r, c) + weight(edge_l - r, c), edge_l > s.m ? edge : s.first};
+            s = {m, s.l * weight(s.m, r, c) + weight(edge_l, r, c), edge_l > s.m ? edge : s.first};
         }
         s = join(s, c, greedy);
         if (lane < C)
@@ -458,7 +473,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         if (lane + 32 < C * kProbsWarps) {
             const Stat t = s_stat[turn][lane + 32];
             const float m = fmaxf(s.m, t.m), r = reference(m);
-            s = {m, s.l * weight(s.m - r, c) + t.l * weight(t.m - r, c),
+            s = {m, s.l * weight(s.m, r, c) + t.l * weight(t.m, r, c),
                  s.m == t.m ? min(s.first, t.first) : s.m > t.m ? s.first : t.first};
         }
         s = join(s, c, greedy);
@@ -514,7 +529,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                 st_checked(dst + edge, edge == s.first ? one : zero);
             continue;
         }
-        const Scale2 c2 = twice(c, reference(s.m));
+        const Scale2 c2 = twice(c, ref_at(c, reference(s.m)));
         // the sum's inverse, NaN for a NaN sum, and what its rounding left, which would
         // be the same for all of the row
         const float inv1 = s.l == 0.0f ? 0.0f : 1.0f / s.l;
