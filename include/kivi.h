@@ -508,7 +508,8 @@ int32_t kivi_token_probs(const void* logits, int32_t dtype, int32_t B,
  * implementation: probabilities are clamped to [0, 1] (NaN to 0), w(r) = r 2^42
  * rounded to an int64 (half to even), products and differences are fp32, each
  * rounded, s is the fp32 rounding of the fp64 quotient, and u_0 is clamped to
- * [0, 1 - 2^-32] (NaN to 0).
+ * [0, 1 - 2^-32] (NaN to 0).  The other u_i are compared as they are: one below 0
+ * accepts a token of which nothing is left, a NaN accepts none.
  *   path[b][0 .. counts[b]) = the kept nodes, 0 first, then -1: the path and
  * counts of kivi_append_path (P = N).  next[b] = the next pending token, -1 if
  * the last node's row of target is all zero.

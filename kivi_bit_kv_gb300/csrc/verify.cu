@@ -349,7 +349,7 @@ verify_tree_kernel(VerifyArgs a, int run)
                     const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
                     upto += lane >= o ? y : 0;
                 }
-                const bool ok = child && !again && t.u[c] < __fmul_rn(r, scale_of(z - (upto - w)));
+                const bool ok = child && t.u[c] < __fmul_rn(r, scale_of(z - (upto - w)));
                 const unsigned hits = __ballot_sync(0xffffffffu, ok);
                 if (hits) {
                     taken = base + __ffs(hits) - 1;
