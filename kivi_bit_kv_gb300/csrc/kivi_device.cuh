@@ -189,11 +189,46 @@ __device__ __forceinline__ T ld_checked(const T* p)
 {
     return KIVI_IN_RANGE(p, sizeof(T)) ? *p : T{};
 }
-// The same through the read-only path (data no kernel of the call writes).
+// The same through the read-only path: data that nothing writes from the kernel's launch to
+// its end.  In a kernel launched as a programmatic dependent that leaves out what an
+// earlier call may have written: such a call may still run at that launch.
 template <class T>
 __device__ __forceinline__ T ldg_checked(const T* p)
 {
     return KIVI_IN_RANGE(p, sizeof(T)) ? __ldg(p) : T{};
+}
+
+// A load, in a kernel launched as a programmatic dependent, of what an earlier call may have
+// written.  Such a call may still run when the kernel is launched, so that the read-only
+// path is not for it; a plain load is held up by each store of the kernel that might go to
+// its address (verification: 17.4 us from 16.8 for 64 chains).  So: a coherent load that
+// stays behind griddepcontrol.wait, as volatile statements do, and is not ordered with the
+// kernel's stores.
+template <class T>
+__device__ __forceinline__ T ld_prior(const T* p)
+{
+    static_assert(sizeof(T) == 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "");
+    T x = {};
+    if (!KIVI_IN_RANGE(p, sizeof(T)))
+        return x;
+    if constexpr (sizeof(T) == 2) {
+        uint16_t v;
+        asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
+        memcpy(&x, &v, 2);
+    } else if constexpr (sizeof(T) == 4) {
+        uint32_t v;
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+        memcpy(&x, &v, 4);
+    } else if constexpr (sizeof(T) == 8) {
+        uint2 v;
+        asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+        memcpy(&x, &v, 8);
+    } else {
+        uint4 v;
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+        memcpy(&x, &v, 16);
+    }
+    return x;
 }
 
 __device__ __forceinline__ uint16_t u4_half(const uint4& v, int k)   // k in [0, 8)

@@ -113,10 +113,10 @@ struct Raw4 {
     __device__ __forceinline__ void load_each(const T* p)
     {
         const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-        v.x = ldg_checked(q) | (uint32_t)ldg_checked(q + 1) << 16;
-        v.y = ldg_checked(q + 2) | (uint32_t)ldg_checked(q + 3) << 16;
+        v.x = ld_prior(q) | (uint32_t)ld_prior(q + 1) << 16;
+        v.y = ld_prior(q + 2) | (uint32_t)ld_prior(q + 3) << 16;
     }
-    __device__ __forceinline__ void load(const T* p) { v = ldg_checked(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void load(const T* p) { v = ld_prior(reinterpret_cast<const uint2*>(p)); }
     // Four of the eight logits of a and b, from number `skip` (1 to 3) on.
     __device__ __forceinline__ void shifted(const Raw4& a, const Raw4& b, int skip)
     {
@@ -150,9 +150,9 @@ struct Raw4<float> {
     static constexpr int BYTES = 16;
     __device__ __forceinline__ void load_each(const float* p)
     {
-        v = make_float4(ldg_checked(p), ldg_checked(p + 1), ldg_checked(p + 2), ldg_checked(p + 3));
+        v = make_float4(ld_prior(p), ld_prior(p + 1), ld_prior(p + 2), ld_prior(p + 3));
     }
-    __device__ __forceinline__ void load(const float* p) { v = ld_nc_f4(p); }
+    __device__ __forceinline__ void load(const float* p) { v = ld_prior(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void clear() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ float2 pair(int i) const { return i ? make_float2(v.z, v.w) : make_float2(v.x, v.y); }
 };
@@ -263,7 +263,7 @@ struct Kept {
             T* to = reinterpret_cast<T*>(slots + slot);
             for (int i = 0; i < 4; ++i)
                 if (x + i >= 0 && x + i < V)
-                    to[i] = ldg_checked(row + x + i);
+                    to[i] = ld_prior(row + x + i);
         }
     }
     // vectors n + tid, n + tid + kProbsThreads .. below end
@@ -371,9 +371,9 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         if (r.on) {
             const int b = row / a.N, i = row % a.N;
             r.src = static_cast<const T*>(a.logits) + b * a.batch_stride + i * a.row_stride;
-            r.on = !(a.n_rows && i >= ldg_checked(a.n_rows + b));
+            r.on = !(a.n_rows && i >= ld_prior(a.n_rows + b));
             if (a.temperature)
-                r.temperature = ldg_checked(a.temperature + b);
+                r.temperature = ld_prior(a.temperature + b);
         }
         return r;
     };
@@ -391,7 +391,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         next = row_of(row + stride);
         const int edge = 4 * nvec + tid;  // one of the logits after the vectors
         const bool has_edge = now.on && rank == C - 1 && edge < V;
-        const float edge_l = has_edge ? to_float(ldg_checked(src + edge)) : -INFINITY;
+        const float edge_l = has_edge ? to_float(ld_prior(src + edge)) : -INFINITY;
         const bool greedy = now.temperature <= 0.0f;
         const Scale c = inverse_temperature(greedy ? 1.0f : now.temperature);
         const int skip = Kept<T>::skip_of(src);

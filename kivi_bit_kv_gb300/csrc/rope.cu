@@ -125,7 +125,7 @@ norm_rope_kernel(const __grid_constant__ RopeArgs a)
     const int token = (int)(w % tokens), b = token / a.N, i = token % a.N;
     const int qk = a.g[0].steps + a.g[1].steps, all = qk + a.g[2].steps;
     const int first = (int)min(w / tokens * a.per, (long long)all), end = min(first + a.per, all);
-    if (first >= end || (a.n_tok && i >= ldg_checked(a.n_tok + b)))
+    if (first >= end || (a.n_tok && i >= ld_prior(a.n_tok + b)))
         return;
     const int half = a.rot / 2, j = lane % L, hl = lane / L;
     // channels of the lane's vectors, and of their first pair in the table of turns
@@ -155,19 +155,19 @@ norm_rope_kernel(const __grid_constant__ RopeArgs a)
         const T* src = static_cast<const T*>(g.in) + (b * g.sequence + i * g.token + h * g.head);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            x[v].raw = ld_nc(src + chan[v]);
+            x[v].raw = ld_prior(reinterpret_cast<const uint4*>(src + chan[v]));
     };
     Vec<T> next[NV];
     load(first, next);
     if (first < qk && half > 0) {
-        const int base = a.base ? ldg_checked(a.base + b) : 0;
+        const int base = a.base ? ld_prior(a.base + b) : 0;
         for (int p = lane; p < half; p += 32) {
             int at = i;
             if (a.pos) {
-                const int ax = a.axis ? min(max(ldg_checked(a.axis + p), 0), a.n_axes - 1) : 0;
-                at = ldg_checked(a.pos + (size_t)ax * tokens + token);
+                const int ax = a.axis ? min(max(ld_prior(a.axis + p), 0), a.n_axes - 1) : 0;
+                at = ld_prior(a.pos + (size_t)ax * tokens + token);
             }
-            const float2 cs = turn((int)((unsigned)at + (unsigned)base), ldg_checked(a.inv_freq + p));
+            const float2 cs = turn((int)((unsigned)at + (unsigned)base), ld_prior(a.inv_freq + p));
             s_cos[warp][p] = cs.x;
             s_sin[warp][p] = cs.y;
         }
@@ -197,7 +197,7 @@ norm_rope_kernel(const __grid_constant__ RopeArgs a)
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int k = 0; k < HW; k += 2) {
-                    const float4 wt = ld_nc_f4(g.weight + chan[v] + 2 * k);
+                    const float4 wt = ld_prior(reinterpret_cast<const float4*>(g.weight + chan[v] + 2 * k));
                     y[v][k] = mul2(y[v][k], mul2(r, pack2(wt.x, wt.y)));
                     y[v][k + 1] = mul2(y[v][k + 1], mul2(r, pack2(wt.z, wt.w)));
                 }

@@ -135,13 +135,13 @@ __device__ __forceinline__ float4 load_edge(const float* row, const Row& at, int
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int end = min(at.end, y1);
     if (y >= at.off && y < end)
-        v.x = ldg_checked(row + y);
+        v.x = ld_prior(row + y);
     if (y + 1 >= at.off && y + 1 < end)
-        v.y = ldg_checked(row + y + 1);
+        v.y = ld_prior(row + y + 1);
     if (y + 2 >= at.off && y + 2 < end)
-        v.z = ldg_checked(row + y + 2);
+        v.z = ld_prior(row + y + 2);
     if (y + 3 >= at.off && y + 3 < end)
-        v.w = ldg_checked(row + y + 3);
+        v.w = ld_prior(row + y + 3);
     return v;
 }
 
@@ -156,11 +156,11 @@ __device__ __forceinline__ void load_lines(const Row& at, int y, int y1, const f
     if (y >= at.off && y + 128 * U <= min(at.end, y1)) {  // all loads at once
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            p[i] = ld_nc_f4(at.p + mine + i * 128);
+            p[i] = ld_prior(reinterpret_cast<const float4*>(at.p + mine + i * 128));
         if (both)
 #pragma unroll
             for (int i = 0; i < U; ++i)
-                q[i] = ld_nc_f4(at.q + mine + i * 128);
+                q[i] = ld_prior(reinterpret_cast<const float4*>(at.q + mine + i * 128));
     } else {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -229,18 +229,18 @@ verify_tree_kernel(VerifyArgs a, int run)
     };
     if (rank == 0) {
         VerifyTree& t = sm.tree;
-        const int n = a.n_draft ? min(max(ldg_checked(a.n_draft + b), 0), N) : N;
+        const int n = a.n_draft ? min(max(ld_prior(a.n_draft + b), 0), N) : N;
         for (int i = tid; i < N; i += threads) {
-            int par = i ? ldg_checked(a.parent + row0 + i) : -1;
-            const int x = i ? ldg_checked(a.tokens + row0 + i) : -1;
+            int par = i ? ld_prior(a.parent + row0 + i) : -1;
+            const int x = i ? ld_prior(a.tokens + row0 + i) : -1;
             if (par < 0 || par >= i || x < 0 || x >= V)
                 par = -1;
             t.parent[i] = par;
             t.token[i] = x;
-            t.u[i] = ldg_checked(a.u + row0 + i);
+            t.u[i] = ld_prior(a.u + row0 + i);
             if (par >= 0 && i < n) {
-                t.p[i] = clamp01(ldg_checked(a.target + (row0 + par) * V + x));
-                t.q[i] = drawn ? clamp01(ldg_checked(a.draft + (row0 + par) * V + x)) : 1.0f;
+                t.p[i] = clamp01(ld_prior(a.target + (row0 + par) * V + x));
+                t.q[i] = drawn ? clamp01(ld_prior(a.draft + (row0 + par) * V + x)) : 1.0f;
             }
         }
         if (tid == 0)
