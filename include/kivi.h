@@ -424,8 +424,8 @@ int32_t kivi_append_path(const kivi_cache* c, const uint16_t* k,
  * Arguments of kivi_norm_rope: N tokens per sequence.  Inputs have the
  * channels of a head side by side; strides of sequences, tokens and heads are
  * in elements, so that views into one projection's output serve as well as
- * tensors of their own.  Strides (of dimensions larger than one) and
- * pointers are multiples of 16 bytes.  An input and its output may both
+ * tensors of their own.  Strides (of dimensions larger than one, of either sign)
+ * and pointers are multiples of 16 bytes.  An input and its output may both
  * be NULL: that group of heads is left out (not all three).
  */
 typedef struct kivi_heads {
@@ -476,8 +476,8 @@ int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream);
  *   probs[b][i][x] = exp((l_x - max_y l_y) / T_b) / sum_z exp((l_z - max_y l_y) / T_b)
  * with T = temperature (fp32 [B], or NULL: 1 everywhere).  T_b <= 0 puts all on the
  * largest logit, the first among equal ones.  logits: B x N rows of V values of
- * type dtype, strides of sequences and rows in elements (any: a padded vocabulary,
- * rows that start at odd elements); probs: fp32 [B][N][V]; 1 <= V <=
+ * type dtype, strides of sequences and rows in elements (any, of either sign: a
+ * padded vocabulary, rows that start at odd elements); probs: fp32 [B][N][V]; 1 <= V <=
  * KIVI_MAX_VOCAB.  n_rows (int32 [B], or NULL: N everywhere) is taken as
  * min(n_rows[b], N) (0 if negative): rows from there on are neither read nor
  * written.  fp32 arithmetic.  A row of -infinity alone is 0; a row with a NaN or

@@ -473,21 +473,6 @@ static int32_t check_aligned4(const void* p, const char* name)  // NULL is fine
     return ((uintptr_t)p & 3u) ? fail(KIVI_EINVAL, "%s is not 4-byte aligned", name) : KIVI_OK;
 }
 
-// Addresses from the first to past the last byte of a tensor; none for NULL.
-struct Span {
-    uintptr_t lo, hi;
-    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
-};
-static Span span_of(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p ? bytes : 0)}; }
-// The same of `run` contiguous elements at each place of n dimensions.
-static Span strided_span(const void* p, const int32_t* dims, const int64_t* strides, int n, int64_t run, int64_t size)
-{
-    int64_t first = 0, last = 0;
-    for (int i = 0; i < n; ++i)
-        (strides[i] < 0 ? first : last) += (dims[i] - 1) * strides[i];
-    return {(uintptr_t)p + (p ? first * size : 0), (uintptr_t)p + (p ? (last + run) * size : 0)};
-}
-
 static int32_t check_dtype(int32_t dtype)
 {
     if (dtype != KIVI_F16 && dtype != KIVI_BF16 && dtype != KIVI_F32)
@@ -549,9 +534,9 @@ int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream)
     const size_t rows = (size_t)c->B * a->N * c->D * 2;
     for (int i = 0; i < 3; ++i) {
         const int32_t dims[3] = {c->B, a->N, heads[i]};
-        const Span in = strided_span(ins[i], dims, strides[i], 3, c->D, a->dtype == KIVI_F32 ? 4 : 2);
+        const kivi::Span in = kivi::strided_span(ins[i], dims, strides[i], 3, c->D, a->dtype == KIVI_F32 ? 4 : 2);
         for (int o = 0; o < 3; ++o)
-            if (in.meets(span_of(outs[o], rows * heads[o])))
+            if (in.meets(kivi::span_of(outs[o], rows * heads[o])))
                 return fail(KIVI_EINVAL, "output %c overlaps input %c_in", "qkv"[o], "qkv"[i]);
     }
     if (a->rot > 0 && (st = check_ptr(a->inv_freq, "inv_freq", false)) != KIVI_OK)
@@ -588,8 +573,8 @@ int32_t kivi_token_probs(const void* logits, int32_t dtype, int32_t B, int32_t N
         return fail(KIVI_EINVAL, "logits is not aligned to its elements");
     const int32_t dims[2] = {B, N};
     const int64_t strides[2] = {batch_stride, row_stride};
-    if (strided_span(logits, dims, strides, 2, V, dtype == KIVI_F32 ? 4 : 2)
-            .meets(span_of(probs, (size_t)B * N * V * sizeof(float))))
+    if (kivi::strided_span(logits, dims, strides, 2, V, dtype == KIVI_F32 ? 4 : 2)
+            .meets(kivi::span_of(probs, (size_t)B * N * V * sizeof(float))))
         return fail(KIVI_EINVAL, "probs overlaps logits");
     if ((st = check_aligned4(temperature, "temperature")) != KIVI_OK ||
         (st = check_aligned4(n_rows, "n_rows")) != KIVI_OK ||

@@ -42,6 +42,22 @@ inline cudaError_t allow_wide_clusters(Kern kern, int (&done)[64])
     return set_attribute_once(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done);
 }
 
+// Addresses from the first to past the last byte of a tensor; none for NULL.
+struct Span {
+    uintptr_t lo, hi;
+    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+inline Span span_of(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p ? bytes : 0)}; }
+// The same of `run` contiguous elements at each place of n dimensions; strides may be
+// negative.
+inline Span strided_span(const void* p, const int32_t* dims, const int64_t* strides, int n, int64_t run, int64_t size)
+{
+    int64_t first = 0, last = 0;
+    for (int i = 0; i < n; ++i)
+        (strides[i] < 0 ? first : last) += (dims[i] - 1) * strides[i];
+    return {(uintptr_t)p + (p ? first * size : 0), (uintptr_t)p + (p ? (last + run) * size : 0)};
+}
+
 // Number of decode chunks (one CTA per KV head and chunk) that cover Tmax.
 int pv_chunks(const kivi_cache& c, int Hq);
 

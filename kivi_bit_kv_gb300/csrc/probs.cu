@@ -582,10 +582,13 @@ token_probs_kernel(ProbsArgs a, int per, int room)
 }
 
 #ifdef KIVI_CHECKS
-static size_t extent(const ProbsArgs& a)
+// The logits that a call may read.
+static CallBuf logits_of(const ProbsArgs& a)
 {
-    const int64_t last = (a.B > 1 ? (a.B - 1) * a.batch_stride : 0) + (a.N > 1 ? (a.N - 1) * a.row_stride : 0) + a.V;
-    return (size_t)last * (a.dtype == KIVI_F32 ? 4 : 2);
+    const int32_t dims[2] = {a.B, a.N};
+    const int64_t strides[2] = {a.batch_stride, a.row_stride};
+    const Span s = strided_span(a.logits, dims, strides, 2, a.V, a.dtype == KIVI_F32 ? 4 : 2);
+    return {reinterpret_cast<const void*>(s.lo), s.hi - s.lo};
 }
 #endif
 
@@ -647,7 +650,7 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
 
 cudaError_t launch_token_probs(const ProbsArgs& a, cudaStream_t s)
 {
-    KIVI_SET_CHECK_BUFFERS(s, {{a.logits, extent(a)}, {a.temperature, (size_t)a.B * 4}, {a.n_rows, (size_t)a.B * 4},
+    KIVI_SET_CHECK_BUFFERS(s, {logits_of(a), {a.temperature, (size_t)a.B * 4}, {a.n_rows, (size_t)a.B * 4},
                                {a.probs, (size_t)a.B * a.N * a.V * 4}});
     switch (a.dtype) {
     case KIVI_F16: return launch_probs<__half>(a, s);

@@ -295,12 +295,12 @@ static cudaError_t launch_rope_d(const kivi_cache& c, const kivi_heads& a, cudaS
 }
 
 #ifdef KIVI_CHECKS
-// Bytes from the first to the last element of a strided input.
-static size_t extent(const kivi_cache& c, const kivi_heads& a, const int64_t* st, int heads)
+// The values of a strided input that a call may read.
+static CallBuf heads_of(const kivi_cache& c, const kivi_heads& a, const void* in, const int64_t* strides, int heads)
 {
-    const int64_t last = (c.B - 1) * st[0] * (c.B > 1) + (a.N - 1) * st[1] * (a.N > 1) +
-                         (heads - 1) * st[2] * (heads > 1) + c.D;
-    return (size_t)last * (a.dtype == KIVI_F32 ? 4 : 2);
+    const int32_t dims[3] = {c.B, a.N, heads};
+    const Span s = strided_span(in, dims, strides, 3, c.D, a.dtype == KIVI_F32 ? 4 : 2);
+    return {reinterpret_cast<const void*>(s.lo), s.hi - s.lo};
 }
 #endif
 
@@ -308,8 +308,8 @@ cudaError_t launch_norm_rope(const kivi_cache& c, const kivi_heads& a, cudaStrea
 {
     const size_t out = (size_t)c.B * a.N * c.D * 2;
     (void)out;
-    KIVI_SET_CHECK_BUFFERS(s, {{a.q_in, extent(c, a, a.q_strides, a.Hq)}, {a.k_in, extent(c, a, a.k_strides, c.H)},
-                               {a.v_in, extent(c, a, a.v_strides, c.H)}, {a.q_weight, (size_t)c.D * 4},
+    KIVI_SET_CHECK_BUFFERS(s, {heads_of(c, a, a.q_in, a.q_strides, a.Hq), heads_of(c, a, a.k_in, a.k_strides, c.H),
+                               heads_of(c, a, a.v_in, a.v_strides, c.H), {a.q_weight, (size_t)c.D * 4},
                                {a.k_weight, (size_t)c.D * 4}, {a.inv_freq, (size_t)a.rot * 2},
                                {a.axis, (size_t)a.rot * 2}, {a.pos, (size_t)a.n_axes * c.B * a.N * 4},
                                {a.base, (size_t)c.B * 4}, {a.n_tok, (size_t)c.B * 4}, {a.q, out * a.Hq},
