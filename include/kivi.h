@@ -463,8 +463,9 @@ typedef struct kivi_heads {
  * the error of an angle stays near 2^-24 for products t below 2^24), rounded to fp16
  * once.  Sums of squares are fp32: a row whose sum exceeds its range gives 0.
  * n_tok[b] is taken as min(n_tok[b], N) (0 if negative): tokens from there on are
- * not read and their rows left as they were.  Only B, H and D of the descriptor
- * are read, and its memory's device is checked.
+ * not read and their rows left as they were.  Hq as for kivi_decode_qk; without
+ * queries it is not read.  The descriptor is checked as in every call; of what it
+ * describes only B, H and D matter here, and the device of its memory.
  */
 int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream);
 

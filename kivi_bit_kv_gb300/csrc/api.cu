@@ -236,10 +236,18 @@ int32_t kivi_append_token(const kivi_cache* c, const uint16_t* k, const uint16_t
     return launched(kivi::launch_append(*c, k, v, status, (cudaStream_t)stream));
 }
 
-static int32_t check_heads(const kivi_cache* c, int32_t Hq)
+static int32_t check_group(const kivi_cache* c, int32_t Hq)
 {
     if (Hq < c->H || Hq % c->H != 0 || Hq / c->H > 16)
         return fail(KIVI_EINVAL, "Hq=%d must be a multiple of H=%d with Hq/H <= 16", Hq, c->H);
+    return KIVI_OK;
+}
+
+static int32_t check_heads(const kivi_cache* c, int32_t Hq)
+{
+    const int32_t st = check_group(c, Hq);
+    if (st != KIVI_OK)
+        return st;
     // one CTA per (b, h, chunk) in a 1-D grid
     const long long ctas = (long long)c->B * c->H * kivi::pv_chunks(*c, Hq);
     if (ctas >= (1ll << 31))
@@ -509,7 +517,7 @@ int32_t kivi_norm_rope(const kivi_cache* c, const kivi_heads* a, void* stream)
         return st;
     if (!a)
         return fail(KIVI_EINVAL, "kivi_heads is NULL");
-    if ((st = check_heads(c, a->Hq)) != KIVI_OK || (st = check_dtype(a->dtype)) != KIVI_OK)
+    if ((a->q_in && (st = check_group(c, a->Hq)) != KIVI_OK) || (st = check_dtype(a->dtype)) != KIVI_OK)
         return st;
     if (a->N < 1 || (long long)c->B * a->N >= (1ll << 27))
         return fail(KIVI_EINVAL, "N=%d: must be >= 1 with B*N < 2^27 tokens", a->N);

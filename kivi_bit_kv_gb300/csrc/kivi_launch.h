@@ -52,10 +52,12 @@ inline Span span_of(const void* p, size_t bytes) { return {(uintptr_t)p, (uintpt
 // negative.
 inline Span strided_span(const void* p, const int32_t* dims, const int64_t* strides, int n, int64_t run, int64_t size)
 {
+    if (!p)
+        return {0, 0};
     int64_t first = 0, last = 0;
     for (int i = 0; i < n; ++i)
         (strides[i] < 0 ? first : last) += (dims[i] - 1) * strides[i];
-    return {(uintptr_t)p + (p ? first * size : 0), (uintptr_t)p + (p ? (last + run) * size : 0)};
+    return {(uintptr_t)p + first * size, (uintptr_t)p + (last + run) * size};
 }
 
 // Number of decode chunks (one CTA per KV head and chunk) that cover Tmax.
