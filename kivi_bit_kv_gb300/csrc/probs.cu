@@ -96,9 +96,13 @@ __device__ __forceinline__ F2 weights(F2 l, const Scale2& c, F2 f, F2 rest)
     const F2 w = mul2(pack2(exp2_ftz(unpack2(y).x), exp2_ftz(unpack2(y).y)), f);
     return fma2(w, fma2(pack2(fmaxf(e.x, -1.0f), fmaxf(e.y, -1.0f)), both(-0.693147181f), rest), w);
 }
-__device__ __forceinline__ float weight(float l, float ref, const Scale& c)
+// The same of one value with f = 1: the factor between sums relative to l and to ref.  Every
+// new maximum waits for it; in single operations it takes 1 to 3 % less of a short row's time.
+__device__ __forceinline__ float weight(float l, Ref ref, const Scale& c)
 {
-    return unpack2(weights(both(l), twice(c, ref_at(c, ref)), both(1.0f), both(0.0f))).x;
+    const float d = __fmaf_rn(l, ref.unit, ref.minus), y = __fmul_rn(d, c.hi);
+    const float e = __fmaf_rn(d, -c.lo, __fmaf_rn(d, -c.hi, y)), w = exp2_ftz(y);
+    return __fmaf_rn(w, __fmul_rn(fmaxf(e, -1.0f), -0.693147181f), w);
 }
 
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -224,7 +228,7 @@ __device__ __forceinline__ Stat join(Stat s, const Scale& c, bool greedy)
 {
     const int top = __reduce_max_sync(0xffffffffu, ordered(s.m + 0.0f));
     const float m = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-    float l = s.l * weight(s.m, reference(m), c);
+    float l = s.l * weight(s.m, ref_at(c, reference(m)), c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -424,9 +428,9 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         auto take = [&](const Raw4<T> (&v)[U], int n) {
             const float m = largest(v);
             if (m > s.m) {
-                s.l *= weight(s.m, m, c);
-                s.m = m;
                 ref = ref_at(c, m);
+                s.l *= weight(s.m, ref, c);
+                s.m = m;
                 if (greedy) {
                     s.first = INT_MAX;
 #pragma unroll
@@ -461,7 +465,8 @@ token_probs_kernel(ProbsArgs a, int per, int room)
             }
         }
         if (has_edge) {  // a thread's last logit
-            const float m = fmaxf(s.m, edge_l), r = reference(m);
+            const float m = fmaxf(s.m, edge_l);
+            const Ref r = ref_at(c, reference(m));
             s = {m, s.l * weight(s.m, r, c) + weight(edge_l, r, c), edge_l > s.m ? edge : s.first};
         }
         s = join(s, c, greedy);
@@ -472,7 +477,8 @@ token_probs_kernel(ProbsArgs a, int per, int room)
         s = lane < C * kProbsWarps ? s_stat[turn][lane] : Stat{-INFINITY, 0.0f, INT_MAX};
         if (lane + 32 < C * kProbsWarps) {
             const Stat t = s_stat[turn][lane + 32];
-            const float m = fmaxf(s.m, t.m), r = reference(m);
+            const float m = fmaxf(s.m, t.m);
+            const Ref r = ref_at(c, reference(m));
             s = {m, s.l * weight(s.m, r, c) + t.l * weight(t.m, r, c),
                  s.m == t.m ? min(s.first, t.first) : s.m > t.m ? s.first : t.first};
         }
@@ -518,6 +524,7 @@ token_probs_kernel(ProbsArgs a, int per, int room)
                 kept.copy(next.src, 0, kept.count);
             const float zero = isnan(s.l) ? s.l : 0.0f, one = s.l == 0.0f ? 0.0f : 1.0f + zero;
             by_alignment([&](auto known) {
+                // (512 rows of 131072 bf16 logits: 73.3 us, 73.8 without unrolling)
 #pragma unroll 4
                 for (int n = 0; n < all; n += kProbsThreads) {
                     const int x = 4 * (j0 + n + tid);
