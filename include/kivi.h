@@ -461,7 +461,11 @@ typedef struct kivi_heads {
  * outside [0, n_axes) is taken as the nearest in it.  Values are converted only.
  * The arithmetic is fp32 with the angle reduced in two terms (any int32 position;
  * the error of an angle stays near 2^-24 for products t below 2^24), rounded to fp16
- * once.  Sums of squares are fp32: a row whose sum exceeds its range gives 0.
+ * once.  Sums of squares are fp32: a row whose sum exceeds its range gives 0, and
+ * squares below 2^-149 count as 0, which is felt where eps is as small.  Cosine and
+ * sine have no factor of their own: where a model scales them, the weights of the
+ * rotated channels can take it, or, with all channels rotated, sm_scale its square;
+ * with some rotated and no weights it is not offered.
  * n_tok[b] is taken as min(n_tok[b], N) (0 if negative): tokens from there on are
  * not read and their rows left as they were.  Hq as for kivi_decode_qk; without
  * queries it is not read.  The descriptor is checked as in every call; of what it

@@ -1,9 +1,10 @@
 // probs.cu -- probabilities of rows of logits, one temperature per sequence
 // (kivi_token_probs).
 //
-// A row is read once, into the shared memory of a cluster of CTAs: each thread keeps a
-// running maximum and sum of its own values, the pairs are joined over the cluster, and
-// the quotients are formed from the values kept.
+// A row is read into the shared memory of a cluster of CTAs: each thread keeps a running
+// maximum and sum of its own values, the pairs are joined over the cluster, and the
+// quotients are formed from the values kept.  What the shared memory of sixteen CTAs does
+// not hold (of rows above 131072 fp32 or 262144 16-bit values) is read again for them.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -610,8 +611,8 @@ static cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s)
         return e;
     // As few CTAs a row as keep all of it; up to eight where fewer leave SMs idle and a
     // thread has more than two vectors; sixteen also where each of them has an SM.  In us
-    // with eight and with sixteen, fp32 rows of 131072: 8 rows 7.7 and 5.4, 512 rows (half
-    // of which eight would read again) 99.6 and 92.5; 32 bf16 rows 7.4 and 8.2.
+    // with eight and with sixteen, fp32 rows of 131072: 8 rows 7.7 and 5.2, 512 rows (half
+    // of which eight would read again) 98.7 and 93.4; 32 bf16 rows 7.6 and 8.4.
     const int rows = a.B * a.N, nvec = a.V / 4;
     int C = 1;
     while (C < kProbsCluster &&

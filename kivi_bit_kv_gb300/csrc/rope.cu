@@ -14,14 +14,18 @@ namespace kivi {
 
 // Four warps a CTA and eight CTAs an SM (64 registers a thread): with 32 warps an SM
 // and one step of each on its way the kernel is bound by DRAM.  In us, for the prompts
-// of a layer (8 x 4096 tokens, 96 heads of 128 channels, fp16) and for 6195 fp32 tokens
-// of 48 heads of 256 channels:
+// of a layer (8 x 4096 tokens, 96 heads of 128 channels, fp16) and for 4260 fp32 tokens
+// of 48 heads of 256 channels, interleaved:
 //     warps a CTA, CTAs an SM, steps on their way    layer    fp32
 //     4, 8, 1                                         246      49.5
 //     4, 7 or 6, 1 (fewer warps, no spills)           254      50.4
 //     8, 4, 1                                         249      50.0
 //     16, 2, 1                                        254      51.1
 //     8, 2, 2                                         294      55.3
+// With pairs of halves the fp32 kernels keep 12 bytes a thread in local memory at 64
+// registers, none with seven CTAs.  In us with eight, seven and six CTAs, for the same
+// fp32 tokens: D = 256 50.2, 50.6, 51.7; D = 128 (96 heads) 50.8, 51.1, 52.2; D = 64
+// (192 heads) 51.6, 50.7, 51.8.
 constexpr int kRopeWarps = 4, kRopeCtas = 8;
 
 // One 16-byte vector of channels: VW of them, as pairs of fp32.
