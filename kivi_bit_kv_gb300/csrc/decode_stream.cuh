@@ -1514,7 +1514,7 @@ decode_stream_kernel(const kivi_cache c, const uint16_t* __restrict__ q, int Hq,
 #pragma unroll
             for (int i = 0; i < QPL; ++i)
                 if (lane + 32 * i < C::QPIECES)
-                    qv[i] = __ldg(q4 + lane + 32 * i);
+                    qv[i] = q4[lane + 32 * i];
         }
         ++o_tiles;
         const int slot = (int)((unsigned long long)k % ns);

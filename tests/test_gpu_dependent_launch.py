@@ -124,3 +124,24 @@ def test_directly_behind_a_kernel_that_lets_the_next_start(cuda, name, captured)
         torch.cuda.synchronize()
         graph.replay() if captured else c.step()
         c.check()
+
+
+def test_decode_behind_the_call_that_writes_its_queries(cuda):
+    """Fused decode, itself a dependent of the call before it, on queries that
+    kivi_norm_rope has just written, over and over."""
+    B, H, gq, D = 4, 2, 4, 128
+    g = torch.Generator(device=cuda).manual_seed(72)
+    cache = make_cache(cuda, B, H, D, 2, 2, 32, 32, [500, 33, 0, 1200], seed=8)
+    q = torch.zeros((B, H * gq, 1, D), dtype=torch.float16, device=cuda)
+    out, want = (torch.zeros((B, H * gq, D), device=cuda) for _ in range(2))
+    ws, f = cache.workspace(H * gq), freqs(D).to(cuda)
+    xs = [torch.randn((B, 1, H * gq, D), generator=g, device=cuda).bfloat16() for _ in range(50)]
+    for x in xs:
+        torch.cuda.synchronize()
+        for y in (xs[0], x):
+            abi.kivi_norm_rope(cache, y, None, None, q, None, None, f, base=cache.lens)
+            abi.kivi_decode_attention(cache, q, out, ws)
+        torch.cuda.synchronize()
+        abi.kivi_decode_attention(cache, q.clone(), want, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
